@@ -4,8 +4,8 @@
  *
  * C ABI.  Every pointer argument is a DEVICE pointer unless stated otherwise,
  * owned by the caller; the library keeps no reference after the call returns
- * and allocates no device memory.  Every call that launches work (the GEMMs
- * and the quantisers) is asynchronous on the given stream (a cudaStream_t
+ * and allocates no device memory.  Every call that launches work (the GEMMs,
+ * the quantisers and the lookups) is asynchronous on the given stream (a cudaStream_t
  * passed as void*; NULL = legacy default stream).
  * Argument checks run synchronously on the host before anything is launched;
  * a call that returns an error status has launched nothing.  There is no CPU
@@ -48,8 +48,9 @@ typedef enum {
   BS_ERR_DEVICE = 6,    /* current device is not an sm_100 (B200-class) GPU */
   BS_ERR_CUDA = 7,      /* a CUDA runtime call failed (launch, encode, ...) */
   BS_ERR_TIMEOUT = 8,   /* a kernel gave up on a bounded wait (bs_get_device_error) */
-  BS_ERR_WORKSPACE = 9  /* workspace smaller than bs_workspace_size(), or a device with more
-                           SMs than bs_int_scaled_mm_noalloc's built-in scratch holds */
+  BS_ERR_WORKSPACE = 9  /* workspace smaller than bs_workspace_size() or
+                           bs_embedding_grad_workspace(), or a device with more SMs than
+                           bs_int_scaled_mm_noalloc's built-in scratch holds */
 } bs_status;
 
 typedef enum {
@@ -363,6 +364,120 @@ bs_status bs_quantize_fp8_t(const void* x, bs_in_dtype x_dtype, int64_t R, int64
 bs_status bs_quantize_fp8_128x128(const void* x, bs_in_dtype x_dtype, int64_t R, int64_t C, int64_t ldx, void* q,
                                   int64_t ldq, void* scale, bs_scale_fmt scale_fmt, int64_t s_rb, int64_t s_cb,
                                   void* stream);
+
+/*
+ * 4-bit matrices with group scales.
+ *
+ * A matrix [N, K] of 4-bit codes c in 0 .. 15, two to a byte: element k of a
+ * row in byte k / 2, even k in the low nibble, row n at q + n*ldq bytes
+ * (ldq >= ceil(K/2)).  Every `group` (32, 64 or 128) consecutive k of a row
+ * share a scale, fp32 or bf16, at scale[n*ld_scale + k/group], and, where
+ * `zero` is given, a zero point in 0 .. 15 at zero[n*ld_zero + k/group] (8
+ * where it is NULL); a row's last group may be short.
+ *   value[n, k] = scale * (c - zero)
+ * Scales are aligned to their element size; ld_scale and ld_zero are at least
+ * ceil(K/group).
+ *
+ * bs_quantize_int4 makes one from x [N, K] (bf16 or fp32, row stride ldx,
+ * aligned to its element size):
+ *   zero NULL:  s = amax / 7,                    c = clamp(rne(x / s), -8, 7) + 8
+ *   otherwise:  lo = min(0, min x), hi = max(0, max x), s = hi / 15 - lo / 15,
+ *               z = clamp(rne(-lo / s), 0, 15),  c = clamp(rne(x / s) + z, 0, 15)
+ * with every quotient and difference rounded to fp32 (bf16 scales: s is then
+ * rounded to bf16, and that s gives z and c), s = 1 where it would be 0, and
+ * rne() the nearest integer, ties to even.  Bit-exact.  Zero is always
+ * represented exactly, and the unused nibble of an odd row's last byte holds
+ * it; bytes past ceil(K/2) are not written.  Non-finite inputs give
+ * unspecified codes.  N == 0 or K == 0 is a no-op.
+ *
+ * bs_dequantize_int4 writes the values, out[n, k] = scale * (c - zero) rounded
+ * to fp32 and then to the output type (BS_OUT_BF16 or BS_OUT_F32, row stride
+ * ldo elements): the operand of a library product when there are more rows
+ * than bs_gemv_int4 takes.
+ */
+bs_status bs_quantize_int4(const void* x, bs_in_dtype x_dtype, int64_t N, int64_t K, int64_t ldx, void* q, int64_t ldq,
+                           void* scale, bs_in_dtype scale_dtype, int64_t ld_scale, uint8_t* zero, int64_t ld_zero,
+                           int32_t group, void* stream);
+bs_status bs_dequantize_int4(const void* q, int64_t ldq, const void* scale, bs_in_dtype scale_dtype, int64_t ld_scale,
+                             const uint8_t* zero, int64_t ld_zero, int32_t group, void* out, bs_out_dtype out_dtype,
+                             int64_t ldo, int64_t N, int64_t K, void* stream);
+
+/*
+ * Product of up to 32 activation rows with a 4-bit matrix (the small-M weight
+ * stream of the scaled GEMMs, for 4-bit weights):
+ *
+ *   out[m, n] = sum_g scale[n, g] * sum_{k in g} x[m, k] * (c[n, k] - zero[n, g]) + bias[n]
+ *
+ * The sum of a group is formed before its scale is applied; sums are fp32, in
+ * an order that depends on the sizes alone, and rounded once to the output
+ * type.  Codes are never rounded and fp32 activations keep all their bits.
+ *   x      bf16 or fp32 [M, K], 1 <= M <= 32, row m at x + m*ldx (ldx >= K),
+ *          aligned to its element size
+ *   q      codes [N, K] as above, 16-byte aligned with ldq a multiple of 16
+ *   bias   fp32 [N] or NULL
+ *   out    [M, N], row stride ldo (>= N), BS_OUT_BF16 or BS_OUT_F32
+ * M == 0 or N == 0 is a no-op; K == 0 writes the bias, or zeros.
+ */
+bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const void* q, int64_t ldq, const void* scale,
+                       bs_in_dtype scale_dtype, int64_t ld_scale, const uint8_t* zero, int64_t ld_zero, int32_t group,
+                       const float* bias, void* out, bs_out_dtype out_dtype, int64_t ldo, int64_t M, int64_t N,
+                       int64_t K, void* stream);
+
+/*
+ * Lookup of table rows, decoded and scaled, and its gradient.
+ *
+ * bs_embedding:       out[t, :] = alpha * table[tokens[t], :]
+ * bs_embedding_grad:  d[v, :]   = alpha * sum_{t: tokens[t] = v} grad[t, :]
+ *
+ * Lookup: an element's value is formed in fp32 (code times scale), multiplied
+ * by alpha in fp32 and rounded to the output type.  A token outside [0, V)
+ * gives a row of zeros.
+ *   tokens   T int32 or int64 numbers, contiguous
+ *   table    [V, D], row v at table + v*ld_table elements:
+ *            BS_TABLE_BF16, BS_TABLE_F32   values; scale, zero and group unused
+ *            BS_TABLE_E4M3, BS_TABLE_E4M3_E8M0  the codes of
+ *              bs_quantize_fp8_1x128, with its scales (fp32 or e8m0 bytes) at
+ *              scale[v*ld_scale + d/128]
+ *            BS_TABLE_INT4  a 4-bit matrix [V, D] as above (ld_table in bytes)
+ *   out      [T, D], row stride ldo (>= D), BS_OUT_BF16 or BS_OUT_F32
+ *
+ * Gradient: every row of d [V, D] is written, rows that no token names with
+ * zeros; with accumulate != 0 the sums are added to d instead (other rows stay
+ * as they are).  Tokens equal to padding_idx (negative: none) or outside
+ * [0, V) contribute nothing.  Sums are fp32 in an order that the tokens alone
+ * decide, so results are deterministic; alpha multiplies the sum, and the
+ * result is rounded once.
+ *   grad     bf16 or fp32 [T, D], row stride ldg (>= D)
+ *   d        [V, D], row stride ldd (>= D), BS_OUT_BF16 or BS_OUT_F32
+ *   workspace  bs_embedding_grad_workspace(T, V, D) bytes, 256-byte aligned;
+ *            its contents need not be set and mean nothing afterwards.  Calls
+ *            that overlap on the GPU need a workspace each.
+ * T and V are below 2^31.  Pointers are aligned to their element sizes (rows
+ * on 16-byte boundaries are faster).  T == 0 or D == 0 looks nothing up; the
+ * gradient of T == 0 is zero.
+ */
+typedef enum {
+  BS_INDEX_I32 = 0,
+  BS_INDEX_I64 = 1
+} bs_index_dtype;
+
+typedef enum {
+  BS_TABLE_BF16 = 0,
+  BS_TABLE_F32 = 1,
+  BS_TABLE_E4M3 = 2,      /* e4m3 codes, fp32 scale per 1x128 group */
+  BS_TABLE_E4M3_E8M0 = 3, /* e4m3 codes, e8m0 scale byte per 1x128 group */
+  BS_TABLE_INT4 = 4       /* 4-bit codes with group scales */
+} bs_table_fmt;
+
+bs_status bs_embedding(const void* tokens, bs_index_dtype token_dtype, int64_t T, const void* table, bs_table_fmt format,
+                       int64_t ld_table, const void* scale, bs_in_dtype scale_dtype, int64_t ld_scale,
+                       const uint8_t* zero, int64_t ld_zero, int32_t group, int64_t V, int64_t D, float alpha, void* out,
+                       bs_out_dtype out_dtype, int64_t ldo, void* stream);
+size_t bs_embedding_grad_workspace(int64_t T, int64_t V, int64_t D);
+bs_status bs_embedding_grad(const void* tokens, bs_index_dtype token_dtype, int64_t T, const void* grad,
+                            bs_in_dtype grad_dtype, int64_t ldg, int64_t V, int64_t D, float alpha, int64_t padding_idx,
+                            void* d, bs_out_dtype d_dtype, int64_t ldd, int32_t accumulate, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* Plan of operation `op` (1 = bs_gemm_fp8_blockwise, 2 = int_scaled_mm,
  * 3 = bmm_a8w8_blockscale, 4 = bs_gemm_fp8_rowwise; G = 1 for ops 1, 2 and 4)

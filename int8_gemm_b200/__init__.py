@@ -14,8 +14,14 @@ calls raise.
     bs_quantize_fp8_1x128(x, scale_format="f32")            -> (q, scale)
     bs_quantize_fp8_t(x, group="128x1", scale_format="f32")  -> (q_t, scale)
     bs_quantize_fp8_128x128(w, scale_format="f32")           -> (q, scale_b)
+    bs_quantize_int4(w, group=128, scale_dtype=torch.float32, asymmetric=False) -> (q, scale, zero)
+    bs_dequantize_int4(q, scale, zero=None, K=None, group=128, out_dtype=torch.bfloat16)
+    bs_gemv_int4(x, q, scale, zero=None, bias=None, group=128, out_dtype=torch.bfloat16)
+    bs_embedding(tokens, table, scale=None, zero=None, format="dense", alpha=1.0, out_dtype=torch.bfloat16)
+    bs_embedding_grad(tokens, grad, num_rows, alpha=1.0, padding_idx=None, out_dtype=torch.float32)
 
-The quantisers are also available as ``quantize_fp8_1x128``, ``quantize_fp8_t`` and ``quantize_fp8_128x128``.
+The quantisers are also available as ``quantize_fp8_1x128``, ``quantize_fp8_t``, ``quantize_fp8_128x128`` and
+``quantize_int4``, the dequantiser as ``dequantize_int4``.
 """
 from __future__ import annotations
 
@@ -83,6 +89,18 @@ def lib() -> ctypes.CDLL:
                       h.bs_gemm_fp8_rowwise, h.bs_quantize_fp8_1x128, h.bs_quantize_fp8_t,
                       h.bs_quantize_fp8_128x128):
                 f.restype = ctypes.c_int
+            cint = ctypes.c_int
+            h.bs_quantize_int4.argtypes = [p, cint, i64, i64, i64, p, i64, p, cint, i64, p, i64, i32, p]
+            h.bs_dequantize_int4.argtypes = [p, i64, p, cint, i64, p, i64, i32, p, cint, i64, i64, i64, p]
+            h.bs_gemv_int4.argtypes = [p, cint, i64, p, i64, p, cint, i64, p, i64, i32, p, p, cint, i64, i64, i64, i64, p]
+            h.bs_embedding.argtypes = [p, cint, i64, p, cint, i64, p, cint, i64, p, i64, i32, i64, i64, ctypes.c_float, p,
+                                       cint, i64, p]
+            h.bs_embedding_grad.argtypes = [p, cint, i64, p, cint, i64, i64, i64, ctypes.c_float, i64, p, cint, i64, i32,
+                                            p, ctypes.c_size_t, p]
+            for f in (h.bs_quantize_int4, h.bs_dequantize_int4, h.bs_gemv_int4, h.bs_embedding, h.bs_embedding_grad):
+                f.restype = ctypes.c_int
+            h.bs_embedding_grad_workspace.argtypes = [i64, i64, i64]
+            h.bs_embedding_grad_workspace.restype = ctypes.c_size_t
             h.bs_status_string.argtypes = [ctypes.c_int]
             h.bs_status_string.restype = ctypes.c_char_p
             h.bs_last_error_message.argtypes = []
@@ -516,9 +534,268 @@ def bs_quantize_fp8_128x128(x: torch.Tensor, scale_format: str = "f32", q: torch
     return q, scale
 
 
+# ---------------------------------------------------------------------------
+# 4-bit matrices with group scales, table lookup and its gradient
+# ---------------------------------------------------------------------------
+_IN_CODE = {torch.bfloat16: 0, torch.float32: 1}  # bs_in_dtype
+
+
+def _same_device(first: torch.Tensor, *others):
+    """The tensors of one call (Nones left out) are CUDA tensors of one device."""
+    for t, name in ((first, "the first argument"), *others):
+        if t is not None:
+            _cuda(t, name)
+            if t.device != first.device:
+                raise BsgemmError(BS_ERR_DEVICE, f"{name} is on {t.device}, the first argument on {first.device}")
+
+
+def _in_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _IN_CODE:
+        raise BsgemmError(BS_ERR_DTYPE, f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return _IN_CODE[t.dtype]
+
+
+def _float_out(dtype: torch.dtype) -> int:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise BsgemmError(BS_ERR_DTYPE, f"out_dtype must be bfloat16 or float32, got {dtype}")
+    return _OUT_CODE[dtype]
+
+
+def _unit_rows(t: torch.Tensor, name: str) -> int:
+    """The row stride of a matrix whose rows are runs of adjacent elements."""
+    if t.dim() != 2:
+        raise BsgemmError(BS_ERR_SHAPE, f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise BsgemmError(BS_ERR_LAYOUT, f"{name} must have unit stride along its rows, got strides {t.stride()}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise BsgemmError(BS_ERR_LAYOUT, f"{name} must have rows that do not overlap, got strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _int4_args(q, scale, zero, K: int, group: int):
+    """(rows, arguments from q to group) of a 4-bit matrix of K columns."""
+    if q.dtype != torch.uint8:
+        raise BsgemmError(BS_ERR_DTYPE, f"q must hold packed 4-bit codes (uint8), got {q.dtype}")
+    if group not in (32, 64, 128):
+        raise BsgemmError(BS_ERR_SHAPE, f"group must be 32, 64 or 128, got {group}")
+    ldq, lds = _unit_rows(q, "q"), _unit_rows(scale, "scale")
+    N, G = q.shape[0], -(-K // group)
+    if q.shape[1] != (K + 1) // 2:
+        raise BsgemmError(BS_ERR_SHAPE, f"q must be [N, {(K + 1) // 2}] for K={K}, got {tuple(q.shape)}")
+    if tuple(scale.shape) != (N, G):
+        raise BsgemmError(BS_ERR_SHAPE, f"scale must be [{N}, {G}], got {tuple(scale.shape)}")
+    ldz = 0
+    if zero is not None:
+        if zero.dtype != torch.uint8:
+            raise BsgemmError(BS_ERR_DTYPE, f"zero must be uint8, got {zero.dtype}")
+        ldz = _unit_rows(zero, "zero")
+        if tuple(zero.shape) != (N, G):
+            raise BsgemmError(BS_ERR_SHAPE, f"zero must be [{N}, {G}], got {tuple(zero.shape)}")
+    return N, (_ptr(q), ldq, _ptr(scale), _in_code(scale, "scale"), lds, _ptr(zero), ldz, group)
+
+
+def _rows_out(out, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
+    """`out`, or a new tensor of `shape` whose rows start on 16-byte boundaries."""
+    if out is None:
+        return _empty_out(shape[:-1], shape[-1], dtype, device)
+    _cuda(out, "out")
+    if out.device != device:
+        raise BsgemmError(BS_ERR_DEVICE, f"out is on {out.device}, the inputs on {device}")
+    if out.dtype != dtype or tuple(out.shape) != shape:
+        raise BsgemmError(BS_ERR_SHAPE, f"out must be {list(shape)} of {dtype}, got {list(out.shape)} of {out.dtype}")
+    return out
+
+
+def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype = torch.float32,
+                     asymmetric: bool = False, q: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                     zero: torch.Tensor | None = None):
+    """Quantisation of x [N, K] (bf16 or fp32, unit stride along K) to 4-bit codes with one scale per row and
+    `group` (32, 64 or 128) consecutive elements: (q, scale, zero).
+
+    q     uint8 [N, ceil(K/2)], two codes to a byte, the even element in the low nibble
+    scale `scale_dtype` (float32 or bfloat16) [N, ceil(K/group)]
+    zero  uint8 [N, ceil(K/group)] if `asymmetric`, else None (8)
+    An element stands for scale * (code - zero).  Symmetric: scale = amax / 7, codes 1 .. 15.  Asymmetric: the
+    range from min(0, min x) to max(0, max x) in 15 steps.
+    """
+    _same_device(x, (q, "q"), (scale, "scale"), (zero, "zero"))
+    xd, ldx = _in_code(x, "x"), _unit_rows(x, "x")
+    if scale_dtype not in _IN_CODE:
+        raise BsgemmError(BS_ERR_DTYPE, f"scale_dtype must be bfloat16 or float32, got {scale_dtype}")
+    if zero is not None and not asymmetric:
+        raise BsgemmError(BS_ERR_SHAPE, "zero points belong to an asymmetric quantisation")
+    if group not in (32, 64, 128):
+        raise BsgemmError(BS_ERR_SHAPE, f"group must be 32, 64 or 128, got {group}")
+    N, K = x.shape
+    G = -(-K // group)
+    q = _empty_out((N,), (K + 1) // 2, torch.uint8, x.device) if q is None else q
+    scale = torch.empty((N, G), dtype=scale_dtype, device=x.device) if scale is None else scale
+    if asymmetric and zero is None:
+        zero = torch.empty((N, G), dtype=torch.uint8, device=x.device)
+    if scale.dtype != scale_dtype:
+        raise BsgemmError(BS_ERR_DTYPE, f"scale must be {scale_dtype}, got {scale.dtype}")
+    n, (qp, ldq, sp, sd, lds, zp, ldz, _) = _int4_args(q, scale, zero, K, group)
+    if n != N:
+        raise BsgemmError(BS_ERR_SHAPE, f"q must have {N} rows, got {n}")
+    with torch.cuda.device(x.device):
+        _check(lib().bs_quantize_int4(_ptr(x), xd, N, K, ldx, qp, ldq, sp, sd, lds, zp, ldz, group, _stream(x.device)))
+    return q, scale, zero
+
+
+def bs_dequantize_int4(q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None, K: int | None = None,
+                       group: int = 128, out_dtype: torch.dtype = torch.bfloat16,
+                       out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values [N, K] of a 4-bit matrix (bs_quantize_int4), scale * (code - zero), as bfloat16 or float32.
+    K is twice q's columns unless given (an odd K leaves the last byte's high nibble unused)."""
+    _same_device(q, (scale, "scale"), (zero, "zero"))
+    K = 2 * q.shape[-1] if K is None else int(K)
+    N, w = _int4_args(q, scale, zero, K, group)
+    code = _float_out(out_dtype)
+    out = _rows_out(out, (N, K), out_dtype, q.device)
+    with torch.cuda.device(q.device):
+        _check(lib().bs_dequantize_int4(*w, _ptr(out), code, _unit_rows(out, "out"), N, K, _stream(q.device)))
+    return out
+
+
+def bs_gemv_int4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None,
+                 bias: torch.Tensor | None = None, group: int = 128, out_dtype: torch.dtype = torch.bfloat16,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Product of up to 32 activation rows with a 4-bit matrix: out = x @ W^T + bias.
+
+    x     bfloat16 or float32 [M, K], M <= 32, or [K] (then out is [N])
+    q, scale, zero  W [N, K] as bs_quantize_int4 makes it, rows of q on 16-byte boundaries
+    bias  float32 [N] or None;  out_dtype bfloat16 or float32
+    Sums are fp32, and neither weights nor activations are rounded on the way.
+    """
+    _same_device(x, (q, "q"), (scale, "scale"), (zero, "zero"), (bias, "bias"))
+    if x.dim() not in (1, 2):
+        raise BsgemmError(BS_ERR_SHAPE, f"x must be [M, K] or [K], got {tuple(x.shape)}")
+    x2 = x.unsqueeze(0) if x.dim() == 1 else x
+    xd, ldx = _in_code(x, "x"), _unit_rows(x2, "x")
+    M, K = x2.shape
+    N, w = _int4_args(q, scale, zero, K, group)
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or not bias.is_contiguous()):
+        raise BsgemmError(BS_ERR_SHAPE, f"bias must be a contiguous float32 [{N}]")
+    code = _float_out(out_dtype)
+    out = _rows_out(out, (*x.shape[:-1], N), out_dtype, x.device)
+    o2 = out.unsqueeze(0) if out.dim() == 1 else out
+    with torch.cuda.device(x.device):
+        _check(lib().bs_gemv_int4(_ptr(x), xd, ldx, *w, _ptr(bias), _ptr(out), code, _unit_rows(o2, "out"), M, N, K,
+                                  _stream(x.device)))
+    return out
+
+
+_TABLE_DENSE = {torch.bfloat16: 0, torch.float32: 1}  # bs_table_fmt
+_TABLE_E4M3, _TABLE_E4M3_E8M0, _TABLE_INT4 = 2, 3, 4
+
+
+def _tokens_arg(tokens: torch.Tensor):
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise BsgemmError(BS_ERR_DTYPE, f"tokens must be int32 or int64, got {tokens.dtype}")
+    return tokens.contiguous(), 0 if tokens.dtype == torch.int32 else 1
+
+
+def bs_embedding(tokens: torch.Tensor, table: torch.Tensor, scale: torch.Tensor | None = None,
+                 zero: torch.Tensor | None = None, format: str = "dense", dim: int | None = None, group: int = 128,
+                 alpha: float = 1.0, out_dtype: torch.dtype = torch.bfloat16,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows of a table times a factor: out[..., :] = alpha * table[tokens[...], :].
+
+    tokens  int32 or int64, any shape; a token outside the table gives a row of zeros
+    table   format "dense": bfloat16 or float32 [V, D]
+            format "e4m3":  the codes of bs_quantize_fp8_1x128 [V, D] with its scales [V, ceil(D/128)] (fp32, or
+                            e8m0 bytes)
+            format "int4":  the codes of bs_quantize_int4 [V, ceil(D/2)] with its scales and zero points for
+                            `group`; D is twice the columns unless `dim` gives it
+    out     [*tokens.shape, D] of out_dtype (bfloat16 or float32), rows of equal distance
+    """
+    _same_device(tokens, (table, "table"), (scale, "scale"), (zero, "zero"))
+    code = _float_out(out_dtype)
+    tok, td = _tokens_arg(tokens)
+    ld = _unit_rows(table, "table")
+    V, D = table.shape
+    sp, sd, lds, zp, ldz = None, 0, 0, None, 0
+    if format == "int4":
+        D = 2 * D if dim is None else int(dim)
+        if scale is None:
+            raise BsgemmError(BS_ERR_NULL, "an int4 table needs its scales")
+        V, (_, ld, sp, sd, lds, zp, ldz, _) = _int4_args(table, scale, zero, D, group)
+        fmt = _TABLE_INT4
+    elif dim is not None and int(dim) != D:
+        raise BsgemmError(BS_ERR_SHAPE, f"dim={dim}, but the table has {D} columns")
+    elif zero is not None:
+        raise BsgemmError(BS_ERR_SHAPE, f"a table of format {format!r} has no zero points")
+    elif format == "e4m3":
+        _bytes8(table, "table")
+        if table.dtype == torch.int8 or scale is None:
+            raise BsgemmError(BS_ERR_DTYPE, "an e4m3 table holds float8_e4m3fn (or uint8) codes with their scales")
+        fmt = _TABLE_E4M3
+        if scale.dtype != torch.float32:
+            scale, fmt = _e8m0_bytes(scale, "scale"), _TABLE_E4M3_E8M0
+        if tuple(scale.shape) != (V, -(-D // 128)):
+            raise BsgemmError(BS_ERR_SHAPE, f"scale must be [{V}, {-(-D // 128)}], got {tuple(scale.shape)}")
+        sp, lds = _ptr(scale), _unit_rows(scale, "scale")
+    elif format == "dense":
+        if scale is not None:
+            raise BsgemmError(BS_ERR_SHAPE, "a dense table has no scales")
+        _in_code(table, "table")
+        fmt = _TABLE_DENSE[table.dtype]
+    else:
+        raise BsgemmError(BS_ERR_DTYPE, f"unknown table format {format!r}")
+    T = tok.numel()
+    out = _rows_out(out, (*tokens.shape, D), out_dtype, tokens.device)
+    try:
+        o2 = out.view(T, D)
+    except RuntimeError:
+        raise BsgemmError(BS_ERR_LAYOUT, f"out must have rows of equal distance, got strides {out.stride()}") from None
+    with torch.cuda.device(tokens.device):
+        _check(lib().bs_embedding(_ptr(tok), td, T, _ptr(table), fmt, ld, sp, sd, lds, zp, ldz, group, V, D,
+                                  float(alpha), _ptr(out), code, _unit_rows(o2, "out"), _stream(tokens.device)))
+    return out
+
+
+def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, alpha: float = 1.0,
+                      padding_idx: int | None = None, out_dtype: torch.dtype = torch.float32,
+                      out: torch.Tensor | None = None, accumulate: bool = False) -> torch.Tensor:
+    """Gradient of bs_embedding's table: out[v, :] = alpha * sum of grad[t, :] over the tokens t equal to v.
+
+    tokens  int32 or int64, any shape;  grad bfloat16 or float32 [*tokens.shape, D], rows of equal distance
+    out     [num_rows, D] of out_dtype (float32 or bfloat16).  Rows that no token names become zero, or, with
+            `accumulate` (which needs `out`), every sum is added to what is there and other rows stay.
+    Tokens equal to padding_idx or outside the table contribute nothing.  The result is deterministic.
+    """
+    _same_device(tokens, (grad, "grad"), (out, "out"))
+    tok, td = _tokens_arg(tokens)
+    gd, code, V = _in_code(grad, "grad"), _float_out(out_dtype), int(num_rows)
+    if grad.dim() != tokens.dim() + 1 or grad.shape[:-1] != tokens.shape:
+        raise BsgemmError(BS_ERR_SHAPE, f"grad must be [*tokens.shape, D], got {tuple(grad.shape)} for "
+                                        f"{tuple(tokens.shape)}")
+    if V < 0 or (padding_idx is not None and not 0 <= padding_idx < V):
+        raise BsgemmError(BS_ERR_SHAPE, f"num_rows={num_rows} and padding_idx={padding_idx} do not fit")
+    if accumulate and out is None:
+        raise BsgemmError(BS_ERR_NULL, "accumulate adds to out, which must be given")
+    T, D = tok.numel(), grad.shape[-1]
+    try:
+        g2 = grad.view(T, D)
+    except RuntimeError:
+        raise BsgemmError(BS_ERR_LAYOUT, f"grad must have rows of equal distance, got strides {grad.stride()}") from None
+    ldg = _unit_rows(g2, "grad")
+    out = _rows_out(out, (V, D), out_dtype, tokens.device)
+    with torch.cuda.device(tokens.device):
+        n = lib().bs_embedding_grad_workspace(T, V, D)
+        ws = torch.empty(n, dtype=torch.uint8, device=tokens.device)  # the allocator's blocks are 512-byte aligned
+        _check(lib().bs_embedding_grad(_ptr(tok), td, T, _ptr(grad), gd, ldg, V, D, float(alpha),
+                                       -1 if padding_idx is None else int(padding_idx), _ptr(out), code,
+                                       _unit_rows(out, "out"), 1 if accumulate else 0, _ptr(ws), n,
+                                       _stream(tokens.device)))
+    return out
+
+
 quantize_fp8_1x128 = bs_quantize_fp8_1x128
 quantize_fp8_t = bs_quantize_fp8_t
 quantize_fp8_128x128 = bs_quantize_fp8_128x128
+quantize_int4 = bs_quantize_int4
+dequantize_int4 = bs_dequantize_int4
 
 
 def plan_for(op: int, M: int, G: int, N: int, K: int, num_sms: int = 148) -> dict:

@@ -11,6 +11,7 @@
 
 #include "bsgemm.h"
 #include "launch.h"
+#include "lowbit.h"
 #include "quantize.h"
 
 using namespace bsg;
@@ -955,6 +956,34 @@ bs_status bs_int_scaled_mm_noalloc(const int8_t* A, int64_t lda, const int8_t* B
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// the error message and device facts, for the entry points of api_lowbit.cu
+// ---------------------------------------------------------------------------
+namespace bsg {
+
+bs_status api_fail(bs_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+void api_clear() { clear_msg(); }
+
+bs_status api_device(int* sms, uint32_t** err) {
+  DeviceCtx* dc = nullptr;
+  const bs_status st = device_ctx(&dc);
+  if (st != BS_OK) return st;
+  *sms = dc->sms;
+  *err = dc->err;
+  return BS_OK;
+}
+
+bs_status api_launched(cudaError_t e, const char* what) { return check_launch(e, what); }
+
+}  // namespace bsg
 
 // ---------------------------------------------------------------------------
 // zero (or bias) fill, K == 0
