@@ -66,6 +66,8 @@ _handle = None
 def lib() -> ctypes.CDLL:
     """Load libbsgemm.so (raises if it has not been built)."""
     global _handle
+    if _handle is not None:  # set last, when every prototype is in place
+        return _handle
     with _lock:
         if _handle is None:
             if not os.path.exists(LIB_PATH):
@@ -184,7 +186,7 @@ def _bytes8(t: torch.Tensor, name: str) -> torch.Tensor:
 def _empty_out(lead: tuple, N: int, dtype: torch.dtype, device) -> torch.Tensor:
     """Output [*lead, N] whose rows start on 16-byte boundaries (the kernels'
     store alignment): the last dimension is padded in memory, not in shape."""
-    per16 = 16 // torch.empty((), dtype=dtype).element_size()
+    per16 = 16 // dtype.itemsize
     Np = -(-N // per16) * per16
     return torch.empty((*lead, Np), dtype=dtype, device=device)[..., :N]
 
@@ -540,70 +542,106 @@ def bs_quantize_fp8_128x128(x: torch.Tensor, scale_format: str = "f32", q: torch
 _IN_CODE = {torch.bfloat16: 0, torch.float32: 1}  # bs_in_dtype
 
 
-def _same_device(first: torch.Tensor, *others):
-    """The tensors of one call (Nones left out) are CUDA tensors of one device."""
-    for t, name in ((first, "the first argument"), *others):
-        if t is not None:
-            _cuda(t, name)
-            if t.device != first.device:
-                raise BsgemmError(BS_ERR_DEVICE, f"{name} is on {t.device}, the first argument on {first.device}")
+# The helpers below keep a call's host time near that of its launch: these operators take a few microseconds at a
+# decoding step's sizes, so device indices are compared as integers, the device is switched only when it is not the
+# current one, and pointers and the stream go to the library as plain integers.
+def _same_device(first: torch.Tensor, *others) -> int:
+    """The device index of one call's tensors (Nones left out), which must be CUDA tensors of one device."""
+    try:
+        index = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != index:
+                raise BsgemmError(BS_ERR_DEVICE, f"tensors of one call on cuda:{index} and on {t.device}")
+    except AttributeError:
+        raise BsgemmError(BS_ERR_DEVICE, "arguments must be CUDA tensors") from None
+    if index < 0:
+        raise BsgemmError(BS_ERR_DEVICE, "arguments must be CUDA tensors (there is no CPU path)")
+    return index
+
+
+def _launch(index: int, fn, *args):
+    """fn(*args, current stream of the device) with that device current; raises on an error status."""
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != BS_OK:
+        _check(status)
 
 
 def _in_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _IN_CODE:
+    code = _IN_CODE.get(t.dtype)
+    if code is None:
         raise BsgemmError(BS_ERR_DTYPE, f"{name} must be bfloat16 or float32, got {t.dtype}")
-    return _IN_CODE[t.dtype]
+    return code
 
 
 def _float_out(dtype: torch.dtype) -> int:
-    if dtype not in (torch.bfloat16, torch.float32):
+    code = _IN_CODE.get(dtype)
+    if code is None:
         raise BsgemmError(BS_ERR_DTYPE, f"out_dtype must be bfloat16 or float32, got {dtype}")
-    return _OUT_CODE[dtype]
+    return code  # BS_OUT_BF16 and BS_OUT_F32 are BS_IN_BF16's and BS_IN_F32's numbers
 
 
 def _unit_rows(t: torch.Tensor, name: str) -> int:
-    """The row stride of a matrix whose rows are runs of adjacent elements."""
+    """The row stride of a matrix whose rows are runs of adjacent elements and do not overlap."""
     if t.dim() != 2:
         raise BsgemmError(BS_ERR_SHAPE, f"{name} must be a matrix, got shape {tuple(t.shape)}")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    (rows, cols), (ld, unit) = t.shape, t.stride()
+    if unit != 1 and cols > 1:
         raise BsgemmError(BS_ERR_LAYOUT, f"{name} must have unit stride along its rows, got strides {t.stride()}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if ld >= cols:
+        return ld
+    if rows > 1:
         raise BsgemmError(BS_ERR_LAYOUT, f"{name} must have rows that do not overlap, got strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return cols
 
 
 def _int4_args(q, scale, zero, K: int, group: int):
     """(rows, arguments from q to group) of a 4-bit matrix of K columns."""
-    if q.dtype != torch.uint8:
-        raise BsgemmError(BS_ERR_DTYPE, f"q must hold packed 4-bit codes (uint8), got {q.dtype}")
     if group not in (32, 64, 128):
         raise BsgemmError(BS_ERR_SHAPE, f"group must be 32, 64 or 128, got {group}")
+    if q.dtype != torch.uint8:
+        raise BsgemmError(BS_ERR_DTYPE, f"q must hold packed 4-bit codes (uint8), got {q.dtype}")
     ldq, lds = _unit_rows(q, "q"), _unit_rows(scale, "scale")
-    N, G = q.shape[0], -(-K // group)
-    if q.shape[1] != (K + 1) // 2:
+    N, cols = q.shape
+    G = -(-K // group)
+    if cols != (K + 1) // 2:
         raise BsgemmError(BS_ERR_SHAPE, f"q must be [N, {(K + 1) // 2}] for K={K}, got {tuple(q.shape)}")
-    if tuple(scale.shape) != (N, G):
+    if scale.shape != (N, G):
         raise BsgemmError(BS_ERR_SHAPE, f"scale must be [{N}, {G}], got {tuple(scale.shape)}")
-    ldz = 0
+    zp, ldz = None, 0
     if zero is not None:
         if zero.dtype != torch.uint8:
             raise BsgemmError(BS_ERR_DTYPE, f"zero must be uint8, got {zero.dtype}")
-        ldz = _unit_rows(zero, "zero")
-        if tuple(zero.shape) != (N, G):
+        zp, ldz = zero.data_ptr(), _unit_rows(zero, "zero")
+        if zero.shape != (N, G):
             raise BsgemmError(BS_ERR_SHAPE, f"zero must be [{N}, {G}], got {tuple(zero.shape)}")
-    return N, (_ptr(q), ldq, _ptr(scale), _in_code(scale, "scale"), lds, _ptr(zero), ldz, group)
+    return N, (q.data_ptr(), ldq, scale.data_ptr(), _in_code(scale, "scale"), lds, zp, ldz, group)
 
 
-def _rows_out(out, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
+def _rows_out(out, shape: tuple, dtype: torch.dtype, index: int, device) -> torch.Tensor:
     """`out`, or a new tensor of `shape` whose rows start on 16-byte boundaries."""
     if out is None:
+        if shape[-1] * dtype.itemsize % 16 == 0:
+            return torch.empty(shape, dtype=dtype, device=device)
         return _empty_out(shape[:-1], shape[-1], dtype, device)
-    _cuda(out, "out")
-    if out.device != device:
-        raise BsgemmError(BS_ERR_DEVICE, f"out is on {out.device}, the inputs on {device}")
-    if out.dtype != dtype or tuple(out.shape) != shape:
+    if _same_device(out) != index:
+        raise BsgemmError(BS_ERR_DEVICE, f"out is on {out.device}, the inputs on cuda:{index}")
+    if out.dtype != dtype or out.shape != shape:
         raise BsgemmError(BS_ERR_SHAPE, f"out must be {list(shape)} of {dtype}, got {list(out.shape)} of {out.dtype}")
     return out
+
+
+def _flat_rows(t: torch.Tensor, T: int, D: int, name: str) -> int:
+    """The row stride of t [..., D] read as T rows of equal distance."""
+    if t.dim() != 2:
+        try:
+            t = t.view(T, D)
+        except RuntimeError:
+            raise BsgemmError(BS_ERR_LAYOUT, f"{name} must have rows of equal distance, got strides {t.stride()}") from None
+    return _unit_rows(t, name)
 
 
 def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype = torch.float32,
@@ -618,7 +656,7 @@ def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype
     An element stands for scale * (code - zero).  Symmetric: scale = amax / 7, codes 1 .. 15.  Asymmetric: the
     range from min(0, min x) to max(0, max x) in 15 steps.
     """
-    _same_device(x, (q, "q"), (scale, "scale"), (zero, "zero"))
+    index, device = _same_device(x, q, scale, zero), x.device
     xd, ldx = _in_code(x, "x"), _unit_rows(x, "x")
     if scale_dtype not in _IN_CODE:
         raise BsgemmError(BS_ERR_DTYPE, f"scale_dtype must be bfloat16 or float32, got {scale_dtype}")
@@ -628,17 +666,18 @@ def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype
         raise BsgemmError(BS_ERR_SHAPE, f"group must be 32, 64 or 128, got {group}")
     N, K = x.shape
     G = -(-K // group)
-    q = _empty_out((N,), (K + 1) // 2, torch.uint8, x.device) if q is None else q
-    scale = torch.empty((N, G), dtype=scale_dtype, device=x.device) if scale is None else scale
-    if asymmetric and zero is None:
-        zero = torch.empty((N, G), dtype=torch.uint8, device=x.device)
-    if scale.dtype != scale_dtype:
+    if q is None:
+        q = _rows_out(None, (N, (K + 1) // 2), torch.uint8, index, device)
+    if scale is None:
+        scale = torch.empty((N, G), dtype=scale_dtype, device=device)
+    elif scale.dtype != scale_dtype:
         raise BsgemmError(BS_ERR_DTYPE, f"scale must be {scale_dtype}, got {scale.dtype}")
-    n, (qp, ldq, sp, sd, lds, zp, ldz, _) = _int4_args(q, scale, zero, K, group)
-    if n != N:
-        raise BsgemmError(BS_ERR_SHAPE, f"q must have {N} rows, got {n}")
-    with torch.cuda.device(x.device):
-        _check(lib().bs_quantize_int4(_ptr(x), xd, N, K, ldx, qp, ldq, sp, sd, lds, zp, ldz, group, _stream(x.device)))
+    if asymmetric and zero is None:
+        zero = torch.empty((N, G), dtype=torch.uint8, device=device)
+    rows, w = _int4_args(q, scale, zero, K, group)
+    if rows != N:
+        raise BsgemmError(BS_ERR_SHAPE, f"q must have {N} rows, got {rows}")
+    _launch(index, lib().bs_quantize_int4, x.data_ptr(), xd, N, K, ldx, *w)
     return q, scale, zero
 
 
@@ -647,13 +686,12 @@ def bs_dequantize_int4(q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor 
                        out: torch.Tensor | None = None) -> torch.Tensor:
     """The values [N, K] of a 4-bit matrix (bs_quantize_int4), scale * (code - zero), as bfloat16 or float32.
     K is twice q's columns unless given (an odd K leaves the last byte's high nibble unused)."""
-    _same_device(q, (scale, "scale"), (zero, "zero"))
+    index = _same_device(q, scale, zero)
     K = 2 * q.shape[-1] if K is None else int(K)
     N, w = _int4_args(q, scale, zero, K, group)
     code = _float_out(out_dtype)
-    out = _rows_out(out, (N, K), out_dtype, q.device)
-    with torch.cuda.device(q.device):
-        _check(lib().bs_dequantize_int4(*w, _ptr(out), code, _unit_rows(out, "out"), N, K, _stream(q.device)))
+    out = _rows_out(out, (N, K), out_dtype, index, q.device)
+    _launch(index, lib().bs_dequantize_int4, *w, out.data_ptr(), code, _unit_rows(out, "out"), N, K)
     return out
 
 
@@ -667,32 +705,32 @@ def bs_gemv_int4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, zero: to
     bias  float32 [N] or None;  out_dtype bfloat16 or float32
     Sums are fp32, and neither weights nor activations are rounded on the way.
     """
-    _same_device(x, (q, "q"), (scale, "scale"), (zero, "zero"), (bias, "bias"))
-    if x.dim() not in (1, 2):
-        raise BsgemmError(BS_ERR_SHAPE, f"x must be [M, K] or [K], got {tuple(x.shape)}")
-    x2 = x.unsqueeze(0) if x.dim() == 1 else x
+    index = _same_device(x, q, scale, zero, bias)
+    x2 = x if x.dim() != 1 else x.unsqueeze(0)
     xd, ldx = _in_code(x, "x"), _unit_rows(x2, "x")
     M, K = x2.shape
     N, w = _int4_args(q, scale, zero, K, group)
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or not bias.is_contiguous()):
-        raise BsgemmError(BS_ERR_SHAPE, f"bias must be a contiguous float32 [{N}]")
+    bp = None
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous():
+            raise BsgemmError(BS_ERR_SHAPE, f"bias must be a contiguous float32 [{N}]")
+        bp = bias.data_ptr()
     code = _float_out(out_dtype)
-    out = _rows_out(out, (*x.shape[:-1], N), out_dtype, x.device)
-    o2 = out.unsqueeze(0) if out.dim() == 1 else out
-    with torch.cuda.device(x.device):
-        _check(lib().bs_gemv_int4(_ptr(x), xd, ldx, *w, _ptr(bias), _ptr(out), code, _unit_rows(o2, "out"), M, N, K,
-                                  _stream(x.device)))
+    out = _rows_out(out, (M, N) if x2 is x else (N,), out_dtype, index, x.device)
+    ldo = _unit_rows(out if x2 is x else out.unsqueeze(0), "out")
+    _launch(index, lib().bs_gemv_int4, x.data_ptr(), xd, ldx, *w, bp, out.data_ptr(), code, ldo, M, N, K)
     return out
 
 
-_TABLE_DENSE = {torch.bfloat16: 0, torch.float32: 1}  # bs_table_fmt
-_TABLE_E4M3, _TABLE_E4M3_E8M0, _TABLE_INT4 = 2, 3, 4
+_TABLE_E4M3, _TABLE_E4M3_E8M0, _TABLE_INT4 = 2, 3, 4  # bs_table_fmt; bf16 and fp32 tables go by _IN_CODE
+_INDEX_CODE = {torch.int32: 0, torch.int64: 1}  # bs_index_dtype
 
 
 def _tokens_arg(tokens: torch.Tensor):
-    if tokens.dtype not in (torch.int32, torch.int64):
+    code = _INDEX_CODE.get(tokens.dtype)
+    if code is None:
         raise BsgemmError(BS_ERR_DTYPE, f"tokens must be int32 or int64, got {tokens.dtype}")
-    return tokens.contiguous(), 0 if tokens.dtype == torch.int32 else 1
+    return tokens.contiguous(), code
 
 
 def bs_embedding(tokens: torch.Tensor, table: torch.Tensor, scale: torch.Tensor | None = None,
@@ -709,48 +747,45 @@ def bs_embedding(tokens: torch.Tensor, table: torch.Tensor, scale: torch.Tensor 
                             `group`; D is twice the columns unless `dim` gives it
     out     [*tokens.shape, D] of out_dtype (bfloat16 or float32), rows of equal distance
     """
-    _same_device(tokens, (table, "table"), (scale, "scale"), (zero, "zero"))
+    index = _same_device(tokens, table, scale, zero)
     code = _float_out(out_dtype)
     tok, td = _tokens_arg(tokens)
-    ld = _unit_rows(table, "table")
-    V, D = table.shape
     sp, sd, lds, zp, ldz = None, 0, 0, None, 0
     if format == "int4":
-        D = 2 * D if dim is None else int(dim)
         if scale is None:
             raise BsgemmError(BS_ERR_NULL, "an int4 table needs its scales")
+        D = 2 * table.shape[-1] if dim is None else int(dim)
         V, (_, ld, sp, sd, lds, zp, ldz, _) = _int4_args(table, scale, zero, D, group)
         fmt = _TABLE_INT4
-    elif dim is not None and int(dim) != D:
-        raise BsgemmError(BS_ERR_SHAPE, f"dim={dim}, but the table has {D} columns")
-    elif zero is not None:
-        raise BsgemmError(BS_ERR_SHAPE, f"a table of format {format!r} has no zero points")
-    elif format == "e4m3":
-        _bytes8(table, "table")
-        if table.dtype == torch.int8 or scale is None:
-            raise BsgemmError(BS_ERR_DTYPE, "an e4m3 table holds float8_e4m3fn (or uint8) codes with their scales")
-        fmt = _TABLE_E4M3
-        if scale.dtype != torch.float32:
-            scale, fmt = _e8m0_bytes(scale, "scale"), _TABLE_E4M3_E8M0
-        if tuple(scale.shape) != (V, -(-D // 128)):
-            raise BsgemmError(BS_ERR_SHAPE, f"scale must be [{V}, {-(-D // 128)}], got {tuple(scale.shape)}")
-        sp, lds = _ptr(scale), _unit_rows(scale, "scale")
-    elif format == "dense":
-        if scale is not None:
-            raise BsgemmError(BS_ERR_SHAPE, "a dense table has no scales")
-        _in_code(table, "table")
-        fmt = _TABLE_DENSE[table.dtype]
     else:
-        raise BsgemmError(BS_ERR_DTYPE, f"unknown table format {format!r}")
+        ld = _unit_rows(table, "table")
+        V, D = table.shape
+        if dim is not None and int(dim) != D:
+            raise BsgemmError(BS_ERR_SHAPE, f"dim={dim}, but the table has {D} columns")
+        if zero is not None:
+            raise BsgemmError(BS_ERR_SHAPE, f"a table of format {format!r} has no zero points")
+        if format == "dense":
+            if scale is not None:
+                raise BsgemmError(BS_ERR_SHAPE, "a dense table has no scales")
+            fmt = _in_code(table, "table")
+        elif format == "e4m3":
+            if scale is None:
+                raise BsgemmError(BS_ERR_NULL, "an e4m3 table needs its scales")
+            if table.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise BsgemmError(BS_ERR_DTYPE, f"table must be float8_e4m3fn (or its uint8 bytes), got {table.dtype}")
+            fmt = _TABLE_E4M3
+            if scale.dtype != torch.float32:
+                scale, fmt = _e8m0_bytes(scale, "scale"), _TABLE_E4M3_E8M0
+            if scale.shape != (V, -(-D // 128)):
+                raise BsgemmError(BS_ERR_SHAPE, f"scale must be [{V}, {-(-D // 128)}], got {tuple(scale.shape)}")
+            sp, lds = scale.data_ptr(), _unit_rows(scale, "scale")
+        else:
+            raise BsgemmError(BS_ERR_DTYPE, f"unknown table format {format!r}")
     T = tok.numel()
-    out = _rows_out(out, (*tokens.shape, D), out_dtype, tokens.device)
-    try:
-        o2 = out.view(T, D)
-    except RuntimeError:
-        raise BsgemmError(BS_ERR_LAYOUT, f"out must have rows of equal distance, got strides {out.stride()}") from None
-    with torch.cuda.device(tokens.device):
-        _check(lib().bs_embedding(_ptr(tok), td, T, _ptr(table), fmt, ld, sp, sd, lds, zp, ldz, group, V, D,
-                                  float(alpha), _ptr(out), code, _unit_rows(o2, "out"), _stream(tokens.device)))
+    out = _rows_out(out, (*tokens.shape, D), out_dtype, index, tokens.device)
+    ldo = _flat_rows(out, T, D, "out")
+    _launch(index, lib().bs_embedding, tok.data_ptr(), td, T, table.data_ptr(), fmt, ld, sp, sd, lds, zp, ldz, group, V, D,
+            float(alpha), out.data_ptr(), code, ldo)
     return out
 
 
@@ -764,7 +799,7 @@ def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, a
             `accumulate` (which needs `out`), every sum is added to what is there and other rows stay.
     Tokens equal to padding_idx or outside the table contribute nothing.  The result is deterministic.
     """
-    _same_device(tokens, (grad, "grad"), (out, "out"))
+    index, device = _same_device(tokens, grad, out), tokens.device
     tok, td = _tokens_arg(tokens)
     gd, code, V = _in_code(grad, "grad"), _float_out(out_dtype), int(num_rows)
     if grad.dim() != tokens.dim() + 1 or grad.shape[:-1] != tokens.shape:
@@ -775,19 +810,14 @@ def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, a
     if accumulate and out is None:
         raise BsgemmError(BS_ERR_NULL, "accumulate adds to out, which must be given")
     T, D = tok.numel(), grad.shape[-1]
-    try:
-        g2 = grad.view(T, D)
-    except RuntimeError:
-        raise BsgemmError(BS_ERR_LAYOUT, f"grad must have rows of equal distance, got strides {grad.stride()}") from None
-    ldg = _unit_rows(g2, "grad")
-    out = _rows_out(out, (V, D), out_dtype, tokens.device)
-    with torch.cuda.device(tokens.device):
-        n = lib().bs_embedding_grad_workspace(T, V, D)
-        ws = torch.empty(n, dtype=torch.uint8, device=tokens.device)  # the allocator's blocks are 512-byte aligned
-        _check(lib().bs_embedding_grad(_ptr(tok), td, T, _ptr(grad), gd, ldg, V, D, float(alpha),
-                                       -1 if padding_idx is None else int(padding_idx), _ptr(out), code,
-                                       _unit_rows(out, "out"), 1 if accumulate else 0, _ptr(ws), n,
-                                       _stream(tokens.device)))
+    ldg = _flat_rows(grad, T, D, "grad")
+    out = _rows_out(out, (V, D), out_dtype, index, device)
+    h = lib()
+    n = h.bs_embedding_grad_workspace(T, V, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)  # the allocator's blocks are 512-byte aligned
+    _launch(index, h.bs_embedding_grad, tok.data_ptr(), td, T, grad.data_ptr(), gd, ldg, V, D, float(alpha),
+            -1 if padding_idx is None else int(padding_idx), out.data_ptr(), code, _unit_rows(out, "out"),
+            1 if accumulate else 0, ws.data_ptr(), n)
     return out
 
 
