@@ -983,6 +983,12 @@ bs_status api_device(int* sms, uint32_t** err) {
 
 bs_status api_launched(cudaError_t e, const char* what) { return check_launch(e, what); }
 
+bs_status api_map_codes(CUtensorMap* map, const void* q, int64_t bytes, int64_t N, int64_t ldq, uint32_t box_bytes,
+                        uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, static_cast<uint64_t>(bytes), static_cast<uint64_t>(N), 1,
+                   static_cast<uint64_t>(ldq), static_cast<uint64_t>(ldq), box_bytes, box_rows, "q", swizzle);
+}
+
 }  // namespace bsg
 
 // ---------------------------------------------------------------------------

@@ -143,6 +143,7 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
     if (!aligned(x, in_size(x_dtype))) return api_fail(BS_ERR_ALIGNMENT, "x must be aligned to its element size");
     if (!aligned(q, 16) || ldq % 16 != 0)
       return api_fail(BS_ERR_ALIGNMENT, "q must be 16-byte aligned with ldq a multiple of 16");
+    if (ldq >= (int64_t{1} << 40)) return api_fail(BS_ERR_LAYOUT, "ldq must be below 2^40");  // tensor map strides
   }
   int sms = 0;
   uint32_t* err = nullptr;
@@ -163,7 +164,10 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
   p.M = static_cast<int>(M);
   p.N = N;
   p.K = K;
-  return api_launched(launch_gemv_int4(p, sms, cs), "4-bit product launch");
+  CUtensorMap map;
+  st = api_map_codes(&map, q, (K + 1) / 2, N, ldq, kInt4TileBytes, kInt4TileRows, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != BS_OK) return st;
+  return api_launched(launch_gemv_int4(p, map, sms, err, cs), "4-bit product launch");
 }
 
 bs_status bs_embedding(const void* tokens, bs_index_dtype token_dtype, int64_t T, const void* table, bs_table_fmt format,

@@ -9,24 +9,41 @@
 // no weight is ever rounded.  fp32 activations are split into three bf16
 // parts that add up to them exactly, one MMA each.
 //
-// A CTA of 8 warps owns 16 matrix rows and its warps split K.  In a block of
-// 128 k, a thread takes for rows g and g + 8 (g = lane / 4) the four words of
-// 8 codes at k = 32 i + 8 (lane % 4): all lanes' word i lies in the same 32 k,
-// so every MMA sums inside one group whatever the group size.  A word's
-// nibbles j and j + 4 form the MMA's k pairs, and the activations are paired
-// the same way.  The warps' sums meet in shared memory and are added in warp
-// order.
+// A CTA owns 128 matrix rows and a run of 128-deep K blocks, which pass
+// through a ring of stages in shared memory.  One thread fetches a block's
+// codes (128 rows x 64 bytes) with a tensor copy; four staging warps write its
+// activations in the order of the MMA's fragments (fp32 split on the way) and
+// its scales and zero points as (scale, 128 + z) pairs; four warps multiply,
+// 32 rows each, so that a fragment of activations serves two 16-row tiles.
+// In a block a thread takes, for rows g and g + 8 of a tile (g = lane / 4), the
+// word of 8 codes at k = 32 u + 8 (lane % 4) for u = 0 .. 3: all lanes' word u
+// lies in the same 32 k, so every MMA sums inside one group whatever the group
+// size, and under the copy's 64-byte swizzle (16-byte piece c of row r at
+// c ^ (r / 2 % 4)) the lanes' words fall on different banks.  A word's nibbles
+// j and j + 4 form the MMA's k pairs, and the activations are paired the same
+// way.  With few row tiles K is split over the CTAs of a cluster, whose partial
+// tiles meet in distributed shared memory and are added in rank order.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "lowbit.h"
+#include "quantize.h"
 #include "sm100.cuh"
 
 namespace bsg {
 
 namespace {
 
-constexpr int kRows = 16;
-constexpr int kWarps = 8;
+namespace cg = cooperative_groups;
+
+constexpr int kMmaWarps = 4;    // 32 rows each
+constexpr int kStageWarps = 4;  // one 32-k unit of activations and 32 rows of scales each
+constexpr int kThreads = 32 * (kMmaWarps + kStageWarps);
+constexpr int kTiles = 2;  // 16-row tiles per warp
+constexpr int kUnits = 4;  // 32-k units per block
+constexpr int kCodeBytes = kInt4TileRows * kInt4TileBytes;
+constexpr int kPitch = kInt4TileRows + 4;  // floats between the rows of a partial tile
+static_assert(kMmaWarps * kTiles * 16 == kInt4TileRows && kUnits * 16 == kInt4TileBytes, "tile and box agree");
 
 __device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -43,208 +60,315 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int j, uint32_t off) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// The high 16 bits of two fp32 values as a bf16 pair.
-__device__ __forceinline__ uint32_t high_pair(float lo, float hi) {
-  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-}
+// Eight activations of a row, k .. k+7 (zero at or past K), as read.
+template <typename XT>
+struct Eight {
+  uint32_t r[2 * sizeof(XT)];
 
-// Activations k .. k+7 of a row as the MMA's k pairs (j, j + 4), in PARTS bf16
-// parts that add up to them.  A truncated value leaves an exact remainder, so
-// three parts of 8 bits hold an fp32 value whole; a value that is not finite
-// is its own first part (NaN kept a NaN) and leaves no remainder.
-template <typename XT, int PARTS>
-__device__ __forceinline__ void load_pairs(const XT* row, long long k, long long K, bool vec, uint32_t (&b)[PARTS][4]) {
-  if constexpr (sizeof(XT) == 2) {
-    uint32_t r[4] = {};
+  __device__ __forceinline__ void load(const XT* row, long long k, long long K, bool vec) {
     if (vec && k + 8 <= K) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + k));
-      r[0] = u.x, r[1] = u.y, r[2] = u.z, r[3] = u.w;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k + i < K) r[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(row[k + i])) << (16 * (i % 2));
-    }
-    b[0][0] = __byte_perm(r[0], r[2], 0x5410);
-    b[0][1] = __byte_perm(r[0], r[2], 0x7632);
-    b[0][2] = __byte_perm(r[1], r[3], 0x5410);
-    b[0][3] = __byte_perm(r[1], r[3], 0x7632);
-  } else {
-    float v[8];
-    if (vec && k + 8 <= K) {
-      const float4 u0 = __ldg(reinterpret_cast<const float4*>(row + k));
-      const float4 u1 = __ldg(reinterpret_cast<const float4*>(row + k) + 1);
-      v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w, v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = k + i < K ? row[k + i] : 0.f;
+      for (int i = 0; i < static_cast<int>(sizeof(XT)) / 2; ++i) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
+        r[4 * i] = u.x, r[4 * i + 1] = u.y, r[4 * i + 2] = u.z, r[4 * i + 3] = u.w;
+      }
+      return;
     }
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
+    for (int i = 0; i < static_cast<int>(2 * sizeof(XT)); ++i) r[i] = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (p == 0 && v[i] != v[i]) v[i] = __uint_as_float(0x7FC00000u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[p][j] = high_pair(v[j], v[j + 4]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float h = __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
-        v[i] = fabsf(v[i]) <= 3.40282347e38f ? __fsub_rn(v[i], h) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      if (k + i >= K) continue;
+      if constexpr (sizeof(XT) == 2) {
+        r[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(row[k + i])) << (16 * (i % 2));
+      } else {
+        r[i] = __float_as_uint(row[k + i]);
       }
     }
   }
-}
 
-// Four bytes of a row at byte offset `off`; bytes at or past `end` read as 0.
-__device__ __forceinline__ uint32_t load_word(const uint8_t* row, long long off, long long end) {
-  if (off + 4 <= end) return __ldg(reinterpret_cast<const uint32_t*>(row + off));
-  uint32_t w = 0;
-  for (int i = 0; i < 4; ++i)
-    if (off + i < end) w |= static_cast<uint32_t>(row[off + i]) << (8 * i);
-  return w;
-}
+  // The k pairs (j, j + 4) of the bf16 parts that add up to the values, one
+  // uint4 per part.  A truncated value leaves an exact remainder, so three
+  // parts of 8 bits hold an fp32 value whole; a value that is not finite is its
+  // own first part (a NaN kept one) and leaves no remainder.
+  template <int PARTS>
+  __device__ __forceinline__ void pairs(uint4 (&b)[PARTS]) const {
+    if constexpr (PARTS == 1) {
+      b[0] = make_uint4(__byte_perm(r[0], r[2], 0x5410), __byte_perm(r[0], r[2], 0x7632),
+                        __byte_perm(r[1], r[3], 0x5410), __byte_perm(r[1], r[3], 0x7632));
+    } else {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (r[i] & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : r[i];
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        b[p] = make_uint4(__byte_perm(v[0], v[4], 0x7632), __byte_perm(v[1], v[5], 0x7632),
+                          __byte_perm(v[2], v[6], 0x7632), __byte_perm(v[3], v[7], 0x7632));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = __uint_as_float(v[i]), h = __uint_as_float(v[i] & 0xFFFF0000u);
+          v[i] = (v[i] & 0x7F800000u) == 0x7F800000u ? 0u : __float_as_uint(__fsub_rn(f, h));
+        }
+      }
+    }
+  }
+};
 
-// GPB: groups per block of 128 k (1, 2 or 4); NT: tiles of 8 activation rows.
-template <typename XT, typename OutT, int GPB, int NT>
-__global__ void __launch_bounds__(kWarps * 32)
-    gemv_int4_kernel(const Int4Product p, bool xvec) {
-  constexpr int PARTS = sizeof(XT) == 2 ? 1 : 3;
-  __shared__ float red[kWarps][NT][kRows][8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
-  const long long n0 = blockIdx.x * static_cast<long long>(kRows);
+// GPB: groups per 128-deep block (1, 2 or 4); NT: tiles of 8 activation rows.
+template <typename XT, int GPB, int NT>
+struct Config {
+  static constexpr int kParts = sizeof(XT) == 2 ? 1 : 3;
+  static constexpr int kXBytes = kUnits * NT * kParts * 512;  // fragments: 16 bytes per lane
+  static constexpr int kScaleBytes = GPB * kInt4TileRows * 8;
+  static constexpr int kStageBytes = kCodeBytes + kXBytes + kScaleBytes;
+  static constexpr int kStages = 4;
+  static constexpr int kSmem = kStages * kStageBytes + 1024;  // and the alignment of the first stage
+  static_assert(kStages * kStageBytes >= 8 * NT * kPitch * 4, "the partial tile takes the ring's place");
+};
+
+// Grid: S consecutive CTAs (a cluster) per 128-row tile, splitting its K blocks.
+template <typename XT, int GPB, int NT>
+__global__ void __launch_bounds__(kThreads, NT <= 2 && sizeof(XT) == 2 ? 3 : 2)
+    gemv_int4_kernel(const __grid_constant__ CUtensorMap tmq, const Int4Product p, int S, bool xvec, uint32_t* err) {
+  using C = Config<XT, GPB, NT>;
+  constexpr int PARTS = C::kParts;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ int abort_flag;
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % S;
+  const long long n0 = static_cast<long long>(blockIdx.x / S) * kInt4TileRows;
   const int KB = static_cast<int>((p.K + 127) / 128);
-  const int kb_lo = static_cast<int>(static_cast<long long>(KB) * warp / kWarps);
-  const int kb_hi = static_cast<int>(static_cast<long long>(KB) * (warp + 1) / kWarps);
-  const long long bytes = (p.K + 1) / 2;
+  const int kb_lo = static_cast<int>(static_cast<long long>(KB) * rank / S);
+  const int kb_hi = static_cast<int>(static_cast<long long>(KB) * (rank + 1) / S);
 
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1 + kStageWarps);  // the tensor copy's arrival and each staging warp's
+      mbar_init(&empty[s], kMmaWarps);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmq);
+  }
+  __syncthreads();
   grid_dependency_wait();  // every operand may come from the previous kernel in the stream
   grid_launch_dependents();
 
-  const XT* x = static_cast<const XT*>(p.x);
-  bool ok[2];
-  const uint8_t* row[2];
+  float acc[kTiles][NT][4] = {};
+  if (warp < kMmaWarps) {
+    const int gr = lane >> 2, t = lane & 3;
+    const uint32_t row_off = (32 * warp + gr) * kInt4TileBytes + 4 * t;
+    const uint32_t swz = (gr >> 1) & 3;
+    int it = 0;
+    for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+      const int st = it % C::kStages;
+      if (!wait_bounded(&full[st], (it / C::kStages) & 1u, &abort_flag, err, kErrTimeout | kRoleConsumer | kWaitStageFull))
+        break;
+      const uint8_t* codes = ring + st * C::kStageBytes + row_off;
+      const uint4* xs = reinterpret_cast<const uint4*>(ring + st * C::kStageBytes + kCodeBytes) + lane;
+      const uint2* sc = reinterpret_cast<const uint2*>(ring + st * C::kStageBytes + kCodeBytes + C::kXBytes) + 32 * warp + gr;
+      constexpr int kUnitsPerGroup = kUnits / GPB;
+      uint2 so[kTiles][2];  // (scale, 128 + z) of rows gr and gr + 8 of each tile
+      float part[kTiles][NT][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long long n = n0 + gr + 8 * h;
-    ok[h] = n < p.N;
-    row[h] = p.w.q + (ok[h] ? n : 0) * p.w.ldq;
-  }
-  float acc[NT][4] = {};
-  for (int kb = kb_lo; kb < kb_hi; ++kb) {
-    const long long k0 = static_cast<long long>(kb) * 128;
-    uint32_t w[2][4];
-    float s[2][GPB];
-    uint32_t off[2][GPB];
+      for (int u = 0; u < kUnits; ++u) {
+        if (u % kUnitsPerGroup == 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+          for (int i = 0; i < kTiles; ++i) {
+            so[i][0] = sc[(u / kUnitsPerGroup) * kInt4TileRows + 16 * i];
+            so[i][1] = sc[(u / kUnitsPerGroup) * kInt4TileRows + 16 * i + 8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[h][i] = ok[h] ? load_word(row[h], k0 / 2 + 16 * i + 4 * t, bytes) : 0u;
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int g = 0; g < GPB; ++g) {
-        const long long n = n0 + gr + 8 * h, j = static_cast<long long>(kb) * GPB + g;
-        s[h][g] = 0.f;
-        uint32_t z = 8;
-        if (ok[h] && j * p.w.group < p.K) {
-          s[h][g] = p.w.scale_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.w.scale)[n * p.w.lds + j])
-                                   : static_cast<const float*>(p.w.scale)[n * p.w.lds + j];
-          if (p.w.zero) z = p.w.zero[n * p.w.ldz + j] & 15u;
+              for (int e = 0; e < 4; ++e) part[i][j][e] = 0.f;
+          }
         }
-        off[h][g] = (0x4300u + z) * 0x10001u;  // 128 + z twice: one unit of the last place of 128 is 1
+        uint32_t a[kTiles][2][4];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          const uint8_t* c = codes + 16 * i * kInt4TileBytes + ((u ^ swz) << 4);
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(c);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(c + 8 * kInt4TileBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            a[i][h][0] = code_pair(w0, 2 * h, so[i][0].y);
+            a[i][h][1] = code_pair(w1, 2 * h, so[i][1].y);
+            a[i][h][2] = code_pair(w0, 2 * h + 1, so[i][0].y);
+            a[i][h][3] = code_pair(w1, 2 * h + 1, so[i][1].y);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+          for (int c = PARTS - 1; c >= 0; --c) {  // the smallest parts first
+            const uint4 b = xs[((u * NT + j) * PARTS + c) * 32];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+              mma_bf16_16x8x16(part[i][j], a[i][0], b.x, b.y);
+              mma_bf16_16x8x16(part[i][j], a[i][1], b.z, b.w);
+            }
+          }
+        }
+        if (u % kUnitsPerGroup == kUnitsPerGroup - 1) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = fmaf(__uint_as_float(so[i][e / 2].x), part[i][j][e], acc[i][j][e]);
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
     }
-    float part[NT][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      constexpr int kWordsPerGroup = 4 / GPB;
-      const int g = i / kWordsPerGroup;
-      if (i % kWordsPerGroup == 0) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) part[j][e] = 0.f;
-      }
-      const uint32_t a0[4] = {code_pair(w[0][i], 0, off[0][g]), code_pair(w[1][i], 0, off[1][g]),
-                              code_pair(w[0][i], 1, off[0][g]), code_pair(w[1][i], 1, off[1][g])};
-      const uint32_t a1[4] = {code_pair(w[0][i], 2, off[0][g]), code_pair(w[1][i], 2, off[1][g]),
-                              code_pair(w[0][i], 3, off[0][g]), code_pair(w[1][i], 3, off[1][g])};
+  } else {
+    const int a = warp - kMmaWarps;  // unit of activations, and 32 rows of scales
+    const XT* x = static_cast<const XT*>(p.x);
+    const int gr = lane >> 2, t = lane & 3;
+    const long long n = n0 + 32 * a + lane;
+    const bool in_row = n < p.N;
+    // a block's activations and scales are in registers one block ahead
+    Eight<XT> v[NT];
+    float s[GPB];
+    uint32_t z[GPB];
+    auto fetch = [&](int kb) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        uint32_t b[PARTS][4] = {};
-        const int m = gr + 8 * j;
-        if (m < p.M) load_pairs<XT, PARTS>(x + m * p.ldx, k0 + 32 * i + 8 * t, p.K, xvec, b);
+        const int m = 8 * j + gr;
+        v[j].load(x + (m < p.M ? m : 0) * p.ldx, static_cast<long long>(kb) * 128 + 32 * a + 8 * t, m < p.M ? p.K : 0, xvec);
+      }
 #pragma unroll
-        for (int c = PARTS - 1; c >= 0; --c) {  // the smallest parts first
-          mma_bf16_16x8x16(part[j], a0, b[c][0], b[c][1]);
-          mma_bf16_16x8x16(part[j], a1, b[c][2], b[c][3]);
+      for (int g = 0; g < GPB; ++g) {
+        const long long j = static_cast<long long>(kb) * GPB + g;
+        s[g] = 0.f;
+        z[g] = 8;
+        if (in_row && j * p.w.group < p.K) {
+          s[g] = p.w.scale_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.w.scale)[n * p.w.lds + j])
+                                : static_cast<const float*>(p.w.scale)[n * p.w.lds + j];
+          if (p.w.zero) z[g] = p.w.zero[n * p.w.ldz + j] & 15u;
         }
       }
-      if (i % kWordsPerGroup == kWordsPerGroup - 1) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(s[e / 2][g], part[j][e], acc[j][e]);
+    };
+    if (kb_lo < kb_hi) fetch(kb_lo);
+    int it = 0;
+    for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+      const int st = it % C::kStages;
+      if (it >= C::kStages && !wait_bounded(&empty[st], (it / C::kStages - 1) & 1u, &abort_flag, err,
+                                            kErrTimeout | kRoleProducer | kWaitStageEmpty))
+        break;
+      uint8_t* stage = ring + st * C::kStageBytes;
+      if (a == 0 && lane == 0) {
+        mbar_arrive_expect_tx(&full[st], kCodeBytes);
+        tma_load_3d(stage, &tmq, &full[st], kb * kInt4TileBytes, static_cast<int>(n0), 0);
       }
+      uint4* xs = reinterpret_cast<uint4*>(stage + kCodeBytes) + lane;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint4 b[PARTS];
+        v[j].template pairs<PARTS>(b);
+#pragma unroll
+        for (int c = 0; c < PARTS; ++c) xs[((a * NT + j) * PARTS + c) * 32] = b[c];
+      }
+      uint2* sc = reinterpret_cast<uint2*>(stage + kCodeBytes + C::kXBytes) + 32 * a + lane;
+#pragma unroll
+      for (int g = 0; g < GPB; ++g)  // one unit of the last place of bf16's 128 is 1
+        sc[g * kInt4TileRows] = make_uint2(__float_as_uint(s[g]), (0x4300u + z[g]) * 0x10001u);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+      if (kb + 1 < kb_hi) fetch(kb + 1);
     }
+    // a wait that gave up leaves copies in flight: let them land before the CTA retires
+    if (a == 0 && lane == 0 && abort_flag) pause_ns(1000000);
   }
 
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[warp][j][gr + 8 * (e / 2)][2 * t + e % 2] = acc[j][e];
+  // the warps' sums as a partial tile [activation row][matrix row], over the ring
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * kRows * 8; i += kWarps * 32) {
-    // consecutive threads take consecutive output columns
-    const int r = i % kRows, m = i / kRows;
-    const long long n = n0 + r;
-    if (m < p.M && n < p.N) {
-      float y = red[0][m / 8][r][m % 8];
+  float* tile = reinterpret_cast<float*>(ring);
+  if (warp < kMmaWarps) {
+    const int gr = lane >> 2, t = lane & 3;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) y += red[w][m / 8][r][m % 8];
-      if (p.bias) y += p.bias[n];
-      OutT* dst = static_cast<OutT*>(p.out) + m * p.ldo + n;
-      if constexpr (sizeof(OutT) == 2) {
-        *dst = __float2bfloat16_rn(y);
-      } else {
-        *dst = y;
-      }
-    }
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          tile[(8 * j + 2 * t + e % 2) * kPitch + 32 * warp + 16 * i + 8 * (e / 2) + gr] = acc[i][j][e];
   }
+  cg::cluster_group cluster = cg::this_cluster();
+  if (S > 1) cluster.sync();
+  else __syncthreads();
+  // CTA `rank` finishes its share of the activation rows
+  for (int i = threadIdx.x; i < p.M * kInt4TileRows; i += kThreads) {
+    const int m = i / kInt4TileRows, r = i % kInt4TileRows;
+    if (m % S != rank || n0 + r >= p.N) continue;
+    float y = 0.f;
+    if (S > 1) {
+      for (int c = 0; c < S; ++c) y += *cluster.map_shared_rank(tile + m * kPitch + r, c);
+    } else {
+      y = tile[m * kPitch + r];
+    }
+    if (p.bias) y += p.bias[n0 + r];
+    const long long o = m * p.ldo + n0 + r;
+    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+    else static_cast<float*>(p.out)[o] = y;
+  }
+  if (S > 1) cluster.sync();  // a CTA's tile stays until every rank has read it
 }
 
-template <typename XT, typename OutT, int GPB, int NT>
-cudaError_t launch_one(const Int4Product& p, cudaStream_t stream) {
+// K splits of a row tile: enough CTAs for two per SM, at most eight to a
+// cluster, each with two K blocks at least.
+int splits_for(long long tiles, long long blocks, int sms) {
+  int S = 1;
+  while (S < 8 && 2 * S * tiles <= 2LL * sms && blocks >= 4 * S) S *= 2;
+  return S;
+}
+
+template <typename XT, int GPB, int NT>
+cudaError_t launch_one(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
+  using C = Config<XT, GPB, NT>;
+  int per_sm = 0;
+  cudaError_t e = ctas_per_sm_once<gemv_int4_kernel<XT, GPB, NT>>(kThreads, C::kSmem, &per_sm);
+  if (e != cudaSuccess) return e;
   const bool xvec = (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 && (p.ldx * sizeof(XT)) % 16 == 0;
-  cudaLaunchAttribute attr[1];
+  const long long tiles = (p.N + kInt4TileRows - 1) / kInt4TileRows;
+  const int S = splits_for(tiles, (p.K + 127) / 128, sms);
+  cudaLaunchAttribute attr[2];
   // programmatic dependent launch: the prologue may overlap the previous kernel
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.N + kRows - 1) / kRows), 1, 1);
-  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemv_int4_kernel<XT, OutT, GPB, NT>, p, xvec);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemv_int4_kernel<XT, GPB, NT>, q, p, S, xvec, err);
 }
 
-template <typename XT, typename OutT, int GPB>
-cudaError_t launch_tiles(const Int4Product& p, cudaStream_t stream) {
-  if (p.M <= 8) return launch_one<XT, OutT, GPB, 1>(p, stream);
-  return p.M <= 16 ? launch_one<XT, OutT, GPB, 2>(p, stream) : launch_one<XT, OutT, GPB, 4>(p, stream);
+template <typename XT, int GPB>
+cudaError_t launch_tiles(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
+  if (p.M <= 8) return launch_one<XT, GPB, 1>(p, q, sms, err, stream);
+  return p.M <= 16 ? launch_one<XT, GPB, 2>(p, q, sms, err, stream) : launch_one<XT, GPB, 4>(p, q, sms, err, stream);
 }
 
-template <typename XT, typename OutT>
-cudaError_t launch_group(const Int4Product& p, cudaStream_t stream) {
-  if (p.w.group == 128) return launch_tiles<XT, OutT, 1>(p, stream);
-  return p.w.group == 64 ? launch_tiles<XT, OutT, 2>(p, stream) : launch_tiles<XT, OutT, 4>(p, stream);
+template <typename XT>
+cudaError_t launch_group(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
+  if (p.w.group == 128) return launch_tiles<XT, 1>(p, q, sms, err, stream);
+  return p.w.group == 64 ? launch_tiles<XT, 2>(p, q, sms, err, stream) : launch_tiles<XT, 4>(p, q, sms, err, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_gemv_int4(const Int4Product& p, int sms, cudaStream_t stream) {
-  (void)sms;
-  if (p.x_bf16)
-    return p.out_bf16 ? launch_group<__nv_bfloat16, __nv_bfloat16>(p, stream) : launch_group<__nv_bfloat16, float>(p, stream);
-  return p.out_bf16 ? launch_group<float, __nv_bfloat16>(p, stream) : launch_group<float, float>(p, stream);
+cudaError_t launch_gemv_int4(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
+  return p.x_bf16 ? launch_group<__nv_bfloat16>(p, q, sms, err, stream) : launch_group<float>(p, q, sms, err, stream);
 }
 
 }  // namespace bsg

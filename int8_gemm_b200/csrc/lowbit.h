@@ -19,6 +19,10 @@ bs_status api_fail(bs_status st, const char* fmt, ...);
 void api_clear();
 bs_status api_device(int* sms, uint32_t** err);
 bs_status api_launched(cudaError_t e, const char* what);
+// Tensor map of N rows of `bytes` bytes, ldq apart, in boxes of box_bytes x
+// box_rows.
+bs_status api_map_codes(CUtensorMap* map, const void* q, int64_t bytes, int64_t N, int64_t ldq, uint32_t box_bytes,
+                        uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
 // ---- 4-bit matrices ---------------------------------------------------------
 // Codes 0..15 of a matrix [N, K], two to a byte (even k in the low nibble),
@@ -52,7 +56,9 @@ struct Int4Product {
   int M;
   long long N, K;
 };
-cudaError_t launch_gemv_int4(const Int4Product& p, int sms, cudaStream_t stream);
+constexpr int kInt4TileRows = 128;  // matrix rows of a CTA's tile, and
+constexpr int kInt4TileBytes = 64;  // bytes of a row per stage: the box of the tensor map of q (64-byte swizzle)
+cudaError_t launch_gemv_int4(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream);
 
 // ---- lookup -----------------------------------------------------------------
 // out[t, :] = alpha * table[tokens[t], :]; tokens null: row t itself.
