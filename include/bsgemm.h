@@ -416,7 +416,8 @@ bs_status bs_dequantize_int4(const void* q, int64_t ldq, const void* scale, bs_i
  *   q      codes [N, K] as above, 16-byte aligned with ldq a multiple of 16
  *   bias   fp32 [N] or NULL
  *   out    [M, N], row stride ldo (>= N), BS_OUT_BF16 or BS_OUT_F32
- * M == 0 or N == 0 is a no-op; K == 0 writes the bias, or zeros.
+ * K is below 2^30 and ldq below 2^40.  M == 0 or N == 0 is a no-op; K == 0
+ * writes the bias, or zeros.
  */
 bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const void* q, int64_t ldq, const void* scale,
                        bs_in_dtype scale_dtype, int64_t ld_scale, const uint8_t* zero, int64_t ld_zero, int32_t group,

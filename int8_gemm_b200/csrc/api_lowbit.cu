@@ -128,7 +128,7 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
   if (M > kInt4MaxM)
     return api_fail(BS_ERR_SHAPE, "M=%lld: at most %d rows (bs_dequantize_int4 and a GEMM serve more)", (long long)M,
                     kInt4MaxM);
-  if (N > kMaxDim || K > kMaxDim) return api_fail(BS_ERR_SHAPE, "size exceeds 2^31-1");
+  if (N > kMaxDim || K > (kMaxDim >> 1)) return api_fail(BS_ERR_SHAPE, "N exceeds 2^31-1 or K 2^30-1");
   if (!in_known(x_dtype)) return api_fail(BS_ERR_DTYPE, "x must be bf16 or f32");
   if (!out_known(out_dtype)) return api_fail(BS_ERR_DTYPE, "bs_gemv_int4 writes bf16 or f32 only");
   bs_status st = check_int4(q, ldq, scale, scale_dtype, ld_scale, zero, ld_zero, group, N, K);
