@@ -393,7 +393,7 @@ bs_status bs_quantize_fp8_128x128(const void* x, bs_in_dtype x_dtype, int64_t R,
  * bs_dequantize_int4 writes the values, out[n, k] = scale * (c - zero) rounded
  * to fp32 and then to the output type (BS_OUT_BF16 or BS_OUT_F32, row stride
  * ldo elements): the operand of a library product when there are more rows
- * than bs_gemv_int4 takes.
+ * than bs_gemv_int4 takes.  K is below 2^30.
  */
 bs_status bs_quantize_int4(const void* x, bs_in_dtype x_dtype, int64_t N, int64_t K, int64_t ldx, void* q, int64_t ldq,
                            void* scale, bs_in_dtype scale_dtype, int64_t ld_scale, uint8_t* zero, int64_t ld_zero,
@@ -453,7 +453,7 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
  *   workspace  bs_embedding_grad_workspace(T, V, D) bytes, 256-byte aligned;
  *            its contents need not be set and mean nothing afterwards.  Calls
  *            that overlap on the GPU need a workspace each.
- * T and V are below 2^31.  Pointers are aligned to their element sizes (rows
+ * T and V are below 2^31, D below 2^30.  Pointers are aligned to their element sizes (rows
  * on 16-byte boundaries are faster).  T == 0 or D == 0 looks nothing up; the
  * gradient of T == 0 is zero.
  */

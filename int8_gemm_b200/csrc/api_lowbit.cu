@@ -60,6 +60,7 @@ bs_status check_rows_out(const void* out, bs_out_dtype out_dtype, int64_t ldo, i
   if (ldo < D) return api_fail(BS_ERR_LAYOUT, "ldo=%lld < %lld", (long long)ldo, (long long)D);
   if (!extent_ok(T, ldo, 4)) return api_fail(BS_ERR_LAYOUT, "a stride times the number of rows is out of range");
   if (!aligned(out, out_size(out_dtype))) return api_fail(BS_ERR_ALIGNMENT, "out must be aligned to its element size");
+  if (D > (kMaxDim >> 1)) return api_fail(BS_ERR_SHAPE, "rows of more than 2^30-1 elements");
   if (T * ((D + 3) / 4) / 1024 >= kMaxDim) return api_fail(BS_ERR_SHAPE, "more than 2^42 elements");
   return BS_OK;
 }
@@ -82,12 +83,13 @@ bs_status bs_quantize_int4(const void* x, bs_in_dtype x_dtype, int64_t N, int64_
   if (ldx < K) return api_fail(BS_ERR_LAYOUT, "ldx=%lld < K=%lld", (long long)ldx, (long long)K);
   if (!extent_ok(N, ldx, 4)) return api_fail(BS_ERR_LAYOUT, "a stride times the number of rows is out of range");
   if (!aligned(x, in_size(x_dtype))) return api_fail(BS_ERR_ALIGNMENT, "x must be aligned to its element size");
+  if (N * ((K + 1023) / 1024) / 8 >= kMaxDim) return api_fail(BS_ERR_SHAPE, "more than 2^44 elements");
   int sms = 0;
   uint32_t* err = nullptr;
   if ((st = api_device(&sms, &err)) != BS_OK) return st;
   return api_launched(
       launch_quantize_int4(x, x_dtype == BS_IN_BF16, N, K, ldx, static_cast<uint8_t*>(q), ldq, scale,
-                           scale_dtype == BS_IN_BF16, ld_scale, zero, ld_zero, group, sms,
+                           scale_dtype == BS_IN_BF16, ld_scale, zero, ld_zero, group,
                            static_cast<cudaStream_t>(stream)),
       "4-bit quantise launch");
 }

@@ -58,68 +58,122 @@ __device__ __forceinline__ void load16(const InT* row, long long k, long long K,
   }
 }
 
-// The integer nearest to y (ties to even) in the low bits of the result, for
-// |y| < 2^22: 1.5 * 2^23 + y has an ulp of one.
-__device__ __forceinline__ int rne_bits(float y) { return __float_as_int(__fadd_rn(y, 12582912.f)); }
+// a / 7 and a / 15, correctly rounded, by Markstein's correction step (see
+// quotient_rn in group_quant.cuh) where nothing under- or overflows: the
+// divisor's reciprocal is a constant, and every significand was checked.
+template <int DIV>
+__device__ __forceinline__ float over_const(float a) {
+  static_assert(DIV == 7 || DIV == 15, "constants below");
+  constexpr float r = DIV == 7 ? 0x1.24924ap-3f : 0x1.111112p-4f;
+  if (!(fabsf(a) >= 0x1p-100f && fabsf(a) <= 3.40282347e38f)) return __fdiv_rn(a, static_cast<float>(DIV));
+  const float q1 = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q1, static_cast<float>(DIV), a), r, q1);
+}
+
+// The codes of a lane's 16 elements, eight to a word: rne(v / s) + z clamped to
+// 0..15.  Adding 1.5 * 2^23 to a quotient rounds it to an integer, ties to even,
+// in the low bits of the sum, and a further z (an integer) is added exactly; so
+// a code is the low nibble of its sum, and a Horner chain in 16 collects them:
+// the sums' common high bits add up to a constant.  FAST: packed two-wide
+// operations on the fp32 correction step, for scales in its range -- where a
+// symmetric group's quotients lie in [-7.03, 7.03] (7 and half a bf16 step of the
+// scale) and need no clamp; otherwise any scale.
+template <bool ASYM, bool FAST>
+__device__ __forceinline__ void codes16(const float (&v)[16], float s, float z, uint32_t (&w)[2]) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+  float2 q[8];
+  if constexpr (FAST) {
+    const float r = __frcp_rn(s);
+    const float2 r2 = make_float2(r, r), ns2 = make_float2(-s, -s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
+      const float2 q1 = __fmul2_rn(x, r2);
+      q[i] = __ffma2_rn(__ffma2_rn(q1, ns2, x), r2, q1);
+    }
+  } else {
+    const double rinv = __drcp_rn(static_cast<double>(s));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = make_float2(over_scale(v[2 * i], rinv), over_scale(v[2 * i + 1], rinv));
+  }
+  uint32_t c[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (ASYM || !FAST) {  // both ends are integers, so clamping before the rounding is the same
+      q[i].x = fminf(fmaxf(q[i].x, -z), 15.f - z);
+      q[i].y = fminf(fmaxf(q[i].y, -z), 15.f - z);
+    }
+    float2 n;
+    if constexpr (ASYM) {
+      n = __fadd2_rn(__fadd2_rn(q[i], make_float2(kRound, kRound)), make_float2(z, z));
+    } else {
+      n = __fadd2_rn(q[i], make_float2(kRound + 8.f, kRound + 8.f));  // 8 is even: ties go the same way
+    }
+    c[2 * i] = __float_as_uint(n.x);
+    c[2 * i + 1] = __float_as_uint(n.y);
+  }
+  constexpr uint32_t kHigh = 0x4B400000u;  // the bits of 1.5 * 2^23
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t t = c[8 * h + 7];
+#pragma unroll
+    for (int i = 6; i >= 0; --i) t = t * 16u + c[8 * h + i];
+    w[h] = t - kHigh * 0x11111111u;
+  }
+}
 
 template <typename InT, typename ScaleT, bool ASYM, int LANES>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     quantize_int4_kernel(const InT* __restrict__ x, long long N, long long K, long long ldx, uint8_t* __restrict__ q,
                          long long ldq, ScaleT* __restrict__ scale, long long lds, uint8_t* __restrict__ zero,
                          long long ldz) {
   constexpr int kGroup = 16 * LANES;
   const int lane = threadIdx.x & 31;
   const long long per_row = (K + kPasses * kWarpElems - 1) / (kPasses * kWarpElems);
-  const long long items = N * per_row;
-  const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
-  for (long long it = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32; it < items; it += warps) {
-    const long long n = it / per_row;
-    const long long k0 = (it - n * per_row) * (kPasses * kWarpElems) + 16 * lane;
-    const InT* row = x + n * ldx;
-    uint8_t* qrow = q + n * ldq;
-    const bool row_vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
-    float v[kPasses][16];
+  const long long it = blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+  const long long n = it / per_row;
+  if (n >= N) return;  // the whole warp
+  const long long k0 = (it - n * per_row) * (kPasses * kWarpElems) + 16 * lane;
+  const InT* row = x + n * ldx;
+  uint8_t* qrow = q + n * ldq;
+  const bool row_vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+  const bool q_vec = (reinterpret_cast<uintptr_t>(qrow) & 7u) == 0;
+  float v[kPasses][16];
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const long long k = k0 + p * kWarpElems;
-      load16<InT>(row, k, K, row_vec && k + 16 <= K, v[p]);
+  for (int p = 0; p < kPasses; ++p) {
+    const long long k = k0 + p * kWarpElems;
+    load16<InT>(row, k, K, row_vec && k + 16 <= K, v[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const long long k = k0 + p * kWarpElems;
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (ASYM) {
+        lo = fminf(lo, v[p][i]);
+        hi = fmaxf(hi, v[p][i]);
+      } else {
+        hi = fmaxf(hi, fabsf(v[p][i]));
+      }
     }
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const long long k = k0 + p * kWarpElems;
-      float lo = 0.f, hi = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if constexpr (ASYM) {
-          lo = fminf(lo, v[p][i]);
-          hi = fmaxf(hi, v[p][i]);
-        } else {
-          hi = fmaxf(hi, fabsf(v[p][i]));
-        }
-      }
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) {
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        if constexpr (ASYM) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      }
-      float s = ASYM ? __fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f)) : __fdiv_rn(hi, 7.f);
-      if constexpr (sizeof(ScaleT) == 2) s = __bfloat162float(__float2bfloat16_rn(s));
-      if (s == 0.f) s = 1.f;
-      float z = 8.f;  // the code of zero
-      if constexpr (ASYM) {
-        z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
-      }
-      float y[16];
-      code_quotients<16>(v[p], s, y);
-      uint32_t w[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        // rne(y) + z clamped to 0..15: clamping y to [-z, 15 - z] first is the
-        // same, both ends being integers
-        const int c = rne_bits(fminf(fmaxf(y[i], -z), 15.f - z)) + static_cast<int>(z);
-        w[i / 8] |= static_cast<uint32_t>(c & 15) << (4 * (i % 8));
-      }
-      if (k >= K) continue;
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      if constexpr (ASYM) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    }
+    float s = ASYM ? __fsub_rn(over_const<15>(hi), over_const<15>(lo)) : over_const<7>(hi);
+    if constexpr (sizeof(ScaleT) == 2) s = __bfloat162float(__float2bfloat16_rn(s));
+    if (s == 0.f) s = 1.f;
+    float z = 8.f;  // the code of zero
+    if constexpr (ASYM) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
+    uint32_t w[2];
+    if (__all_sync(0xffffffffu, quotient_fast_range(s) && hi <= 3.40282347e38f)) {
+      codes16<ASYM, true>(v[p], s, z, w);
+    } else {
+      codes16<ASYM, false>(v[p], s, z, w);
+    }
+    if (k < K) {
       if (lane % LANES == 0) {
         const long long g = k / kGroup;
         if constexpr (sizeof(ScaleT) == 2) {
@@ -130,7 +184,7 @@ __global__ void __launch_bounds__(kThreads)
         if constexpr (ASYM) zero[n * ldz + g] = static_cast<uint8_t>(z);
       }
       uint8_t* dst = qrow + k / 2;
-      if (k + 16 <= K && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+      if (q_vec && k + 16 <= K) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
       } else {
 #pragma unroll
@@ -143,10 +197,9 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename InT, typename ScaleT, bool ASYM, int LANES>
 cudaError_t launch_one(const void* x, long long N, long long K, long long ldx, uint8_t* q, long long ldq, void* scale,
-                       long long lds, uint8_t* zero, long long ldz, int sms, cudaStream_t stream) {
+                       long long lds, uint8_t* zero, long long ldz, cudaStream_t stream) {
   const long long items = N * ((K + kPasses * kWarpElems - 1) / (kPasses * kWarpElems));
-  long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 8LL * sms) blocks = 8LL * sms;
+  const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
   quantize_int4_kernel<InT, ScaleT, ASYM, LANES><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
       static_cast<const InT*>(x), N, K, ldx, q, ldq, static_cast<ScaleT*>(scale), lds, zero, ldz);
   return cudaGetLastError();
@@ -167,16 +220,16 @@ cudaError_t launch_asym(bool asym, A... a) {
 
 cudaError_t launch_quantize_int4(const void* x, bool x_bf16, long long N, long long K, long long ldx, uint8_t* q,
                                  long long ldq, void* scale, bool scale_bf16, long long lds, uint8_t* zero,
-                                 long long ldz, int group, int sms, cudaStream_t stream) {
+                                 long long ldz, int group, cudaStream_t stream) {
   const bool asym = zero != nullptr;
   if (x_bf16)
     return scale_bf16 ? launch_asym<__nv_bfloat16, __nv_bfloat16>(asym, group, x, N, K, ldx, q, ldq, scale, lds, zero,
-                                                                  ldz, sms, stream)
+                                                                  ldz, stream)
                       : launch_asym<__nv_bfloat16, float>(asym, group, x, N, K, ldx, q, ldq, scale, lds, zero, ldz,
-                                                          sms, stream);
+                                                          stream);
   return scale_bf16
-             ? launch_asym<float, __nv_bfloat16>(asym, group, x, N, K, ldx, q, ldq, scale, lds, zero, ldz, sms, stream)
-             : launch_asym<float, float>(asym, group, x, N, K, ldx, q, ldq, scale, lds, zero, ldz, sms, stream);
+             ? launch_asym<float, __nv_bfloat16>(asym, group, x, N, K, ldx, q, ldq, scale, lds, zero, ldz, stream)
+             : launch_asym<float, float>(asym, group, x, N, K, ldx, q, ldq, scale, lds, zero, ldz, stream);
 }
 
 }  // namespace bsg

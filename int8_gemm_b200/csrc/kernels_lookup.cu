@@ -9,10 +9,9 @@
 // 4-bit matrices uses this kernel, with row t itself in the place of a token.
 // A token outside [0, V) gives a row of zeros and reads nothing.
 //
-// A thread handles pieces of 16 output bytes, consecutive lanes consecutive
-// pieces, four pieces' loads in flight; a block takes a run of consecutive
-// pieces, so the division that finds a piece's row is 32 bits wide whatever
-// the size of the output.
+// A lane handles pieces of 16 output bytes, the lanes of a warp side by side in
+// a row (in several where rows are short), four pieces' loads in flight; a
+// warp stays in its rows, so addresses are worked out once per row.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -23,8 +22,6 @@ namespace bsg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-constexpr int kRun = kThreads * kUnroll;  // pieces per block
 
 enum class Fmt { kBF16, kF32, kE4M3, kE4M3E8M0, kInt4 };
 
@@ -37,93 +34,117 @@ __device__ __forceinline__ long long token_at(const LookupArgs& a, long long t) 
   return a.tokens64 ? static_cast<const long long*>(a.tokens)[t] : static_cast<const int*>(a.tokens)[t];
 }
 
-__device__ __forceinline__ float int4_scale(const Int4Matrix& w, long long r, long long g) {
-  return w.scale_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w.scale)[r * w.lds + g])
-                      : static_cast<const float*>(w.scale)[r * w.lds + g];
-}
+// A table row: where its elements, scales and zero points start.
+template <Fmt F>
+struct Row {
+  const uint8_t *data, *scale, *zero;
+  bool scale_bf16;
+  int group_shift;
 
-// Elements d .. d+E-1 of row r as fp32 (those at or past D are not used).
-// `vec`: the row starts on a 16-byte boundary and the piece lies inside it.
+  __device__ __forceinline__ Row(const LookupArgs& a, long long r) : scale(nullptr), zero(nullptr) {
+    if constexpr (F == Fmt::kInt4) {
+      data = a.w.q + r * a.w.ldq;
+      scale_bf16 = a.w.scale_bf16;
+      scale = static_cast<const uint8_t*>(a.w.scale) + r * a.w.lds * (scale_bf16 ? 2 : 4);
+      if (a.w.zero) zero = a.w.zero + r * a.w.ldz;
+      group_shift = a.group_shift;
+    } else {
+      data = static_cast<const uint8_t*>(a.table) + r * a.ld * (F == Fmt::kBF16 ? 2 : (F == Fmt::kF32 ? 4 : 1));
+      if constexpr (F == Fmt::kE4M3 || F == Fmt::kE4M3E8M0)
+        scale = static_cast<const uint8_t*>(a.scale) + r * a.lds * (F == Fmt::kE4M3 ? 4 : 1);
+    }
+  }
+};
+
+// A piece as read: its bits, and its group's scale (as stored) and zero point.
 template <Fmt F, int E>
-__device__ __forceinline__ void read_piece(const LookupArgs& a, long long r, long long d, bool vec, float (&v)[E]) {
-  if constexpr (F == Fmt::kBF16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.table) + r * a.ld + d;
-    if (vec) {
-      uint32_t w[E / 2];
-      if constexpr (E == 8) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-      } else {
+struct Piece {
+  static constexpr int kBytes = F == Fmt::kF32 ? 4 * E : (F == Fmt::kBF16 ? 2 * E : (F == Fmt::kInt4 ? E / 2 : E));
+  static constexpr int kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords];
+  uint32_t s, z;
+
+  // Elements d .. d+E-1 of the row, `left` of which exist (the bits of the others
+  // are zero).  `vec`: the row starts on a 16-byte boundary.  A piece never
+  // straddles a group (of 32 elements or more).
+  __device__ __forceinline__ void load(const Row<F>& row, int d, int left, bool vec) {
+    const uint8_t* p = row.data + (F == Fmt::kInt4 ? d / 2 : static_cast<long long>(d) * (kBytes / E));
+    if constexpr (F == Fmt::kInt4) {
+      const int g = d >> row.group_shift;
+      s = row.scale_bf16 ? __ldg(reinterpret_cast<const uint16_t*>(row.scale) + g)
+                         : __ldg(reinterpret_cast<const uint32_t*>(row.scale) + g);
+      z = row.zero ? __ldg(row.zero + g) : 8u;
+    }
+    if constexpr (F == Fmt::kE4M3) s = __ldg(reinterpret_cast<const uint32_t*>(row.scale) + (d >> 7));
+    if constexpr (F == Fmt::kE4M3E8M0) s = __ldg(row.scale + (d >> 7));
+    if (vec && left >= E) {
+      if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+      } else if constexpr (kBytes == 8) {
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
         w[0] = u.x, w[1] = u.y;
-      }
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = d + i < a.D ? __bfloat162float(p[i]) : 0.f;
-    }
-  } else if constexpr (F == Fmt::kF32) {
-    const float* p = static_cast<const float*>(a.table) + r * a.ld + d;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
-        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = d + i < a.D ? p[i] : 0.f;
-    }
-  } else if constexpr (F == Fmt::kE4M3 || F == Fmt::kE4M3E8M0) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.table) + r * a.ld + d;
-    uint32_t w[E / 4] = {};
-    if (vec) {
-      if constexpr (E == 8) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-        w[0] = u.x, w[1] = u.y;
-      } else {
+      } else if constexpr (kBytes == 4) {
         w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else {
+        w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
       }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+    if constexpr (F == Fmt::kF32) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i < left) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else if constexpr (F == Fmt::kBF16) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i < left) w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i % 2));
+    } else if constexpr (F == Fmt::kInt4) {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i)
+        if (2 * i < left) w[0] |= static_cast<uint32_t>(p[i]) << (8 * i);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (d + i < a.D) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+        if (i < left) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
     }
-    const long long g = r * a.lds + (d >> 7);  // a piece never straddles a group of 128
-    const float s = F == Fmt::kE4M3 ? static_cast<const float*>(a.scale)[g]
-                                    : e8m0_value(static_cast<const uint8_t*>(a.scale)[g]);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const __half2_raw h =
-          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 4] >> (8 * (i % 4))), __NV_E4M3);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[i] = f.x * s;
-      v[i + 1] = f.y * s;
-    }
-  } else {
-    const uint8_t* p = a.w.q + r * a.w.ldq + d / 2;
-    uint32_t w = 0;
-    if (vec) {
-      w = E == 8 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : __ldg(reinterpret_cast<const uint16_t*>(p));
-    } else {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i)
-        if (d + 2 * i < a.D) w |= static_cast<uint32_t>(p[i]) << (8 * i);
-    }
-    const long long g = d / a.w.group;  // nor one of 32
-    const float s = int4_scale(a.w, r, g);
-    const int z = a.w.zero ? a.w.zero[r * a.w.ldz + g] : 8;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = static_cast<float>(static_cast<int>((w >> (4 * i)) & 15u) - z) * s;
   }
-}
+
+  // Its values in fp32.
+  __device__ __forceinline__ void values(const Row<F>& row, float (&v)[E]) const {
+    if constexpr (F == Fmt::kF32) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (F == Fmt::kBF16) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    } else if constexpr (F == Fmt::kInt4) {
+      const float f = __uint_as_float(row.scale_bf16 ? s << 16 : s);
+      // a nibble in the mantissa of 2^23 gives 2^23 + c; less 2^23 + z, exactly
+      const float off = __uint_as_float(0x4B000000u | (z & 15u));
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = (__uint_as_float(0x4B000000u | ((w[0] >> (4 * i)) & 15u)) - off) * f;
+    } else {
+      const float f = F == Fmt::kE4M3 ? __uint_as_float(s) : e8m0_value(static_cast<uint8_t>(s));
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 4] >> (8 * (i % 4))), __NV_E4M3);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[i] = x.x * f;
+        v[i + 1] = x.y * f;
+      }
+    }
+  }
+};
 
 template <typename OutT, int E>
-__device__ __forceinline__ void write_piece(OutT* p, const float (&v)[E], long long left, bool vec) {
+__device__ __forceinline__ void write_piece(OutT* p, const float (&v)[E], int left, bool vec) {
   if constexpr (sizeof(OutT) == 2) {
     if (vec) {
       uint32_t w[4];
@@ -149,38 +170,44 @@ __device__ __forceinline__ void write_piece(OutT* p, const float (&v)[E], long l
   }
 }
 
-// tvec / ovec: table rows and output rows start on 16-byte boundaries.
-template <Fmt F, typename OutT>
-__global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a, uint32_t pieces, bool tvec, bool ovec) {
+// A warp's item: U pieces per lane of 32 / lpr rows, lpr lanes side by side in
+// a row.  blockIdx.x: kThreads / 32 items' rows; blockIdx.y: the run of U * lpr
+// pieces (gridDim.y runs apart).  tvec / ovec: table rows and output rows start
+// on 16-byte boundaries.
+template <Fmt F, typename OutT, int U>
+__global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a, int lpr_log2, bool tvec, bool ovec) {
   constexpr int E = 16 / sizeof(OutT);
-  const long long total = a.T * static_cast<long long>(pieces);
-  const long long run0 = blockIdx.x * static_cast<long long>(kRun);
-  const long long t0 = run0 / pieces;
-  const uint32_t rem = static_cast<uint32_t>(run0 - t0 * pieces);
-  float v[kUnroll][E];
-  long long t[kUnroll], d[kUnroll];
+  const int lane = threadIdx.x & 31, lpr = 1 << lpr_log2;
+  const long long t = ((blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32) << (5 - lpr_log2)) + (lane >> lpr_log2);
+  if (t >= a.T) return;
+  const long long r = token_at(a, t);
+  const bool named = r >= 0 && r < a.V;
+  const int D = static_cast<int>(a.D);
+  OutT* out = static_cast<OutT*>(a.out) + t * a.ldo;
+  const Row<F> row(a, named ? r : 0);
+  const int step = U * E * lpr;
+  for (long long d0 = static_cast<long long>(blockIdx.y) * step; d0 < D; d0 += static_cast<long long>(gridDim.y) * step) {
+    const int d = static_cast<int>(d0) + E * (lane & (lpr - 1));
+    Piece<F, E> piece[U];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t i = threadIdx.x + u * kThreads;
-    const uint32_t off = rem + i, row = off / pieces;  // rem < pieces < 2^31
-    t[u] = t0 + row;
-    d[u] = static_cast<long long>(off - row * pieces) * E;
-    if (run0 + i >= total) t[u] = -1;
-    if (t[u] < 0) continue;
-    const long long r = token_at(a, t[u]);
-    if (r >= 0 && r < a.V) {
-      read_piece<F, E>(a, r, d[u], tvec && d[u] + E <= a.D, v[u]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      const int at = d + u * E * lpr;
+      if (named && at < D) piece[u].load(row, at, D - at, tvec);
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    if (t[u] < 0) continue;
+    for (int u = 0; u < U; ++u) {
+      const int at = d + u * E * lpr;
+      if (at >= D) break;
+      float v[E] = {};
+      if (named) {
+        piece[u].values(row, v);
+        if (a.alpha != 1.f) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[u][e] *= a.alpha;
-    write_piece<OutT, E>(static_cast<OutT*>(a.out) + t[u] * a.ldo + d[u], v[u], a.D - d[u], ovec && d[u] + E <= a.D);
+          for (int e = 0; e < E; ++e) v[e] *= a.alpha;
+        }
+      }
+      write_piece<OutT, E>(out + at, v, D - at, ovec && D - at >= E);
+    }
   }
 }
 
@@ -188,17 +215,27 @@ bool rows16(const void* base, long long ld_bytes) {
   return (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && ld_bytes % 16 == 0;
 }
 
-template <Fmt F, typename OutT>
-cudaError_t launch_fmt(const LookupArgs& a, cudaStream_t stream) {
+template <Fmt F, typename OutT, int U>
+cudaError_t launch_unroll(const LookupArgs& a, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(OutT);
   const long long pieces = (a.D + E - 1) / E;
-  const long long blocks = (a.T * pieces + kRun - 1) / kRun;
+  int lpr_log2 = 0;
+  while (lpr_log2 < 5 && (1 << lpr_log2) < pieces) ++lpr_log2;
+  const long long rows = static_cast<long long>(kThreads) >> lpr_log2;  // per block
+  const long long runs = (pieces + (U << lpr_log2) - 1) / (U << lpr_log2);
   const bool tvec = F == Fmt::kInt4 ? rows16(a.w.q, a.w.ldq)
                                     : rows16(a.table, a.ld * (F == Fmt::kBF16 ? 2 : F == Fmt::kF32 ? 4 : 1));
   const bool ovec = rows16(a.out, a.ldo * static_cast<long long>(sizeof(OutT)));
-  lookup_kernel<F, OutT><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, static_cast<uint32_t>(pieces),
-                                                                                 tvec, ovec);
+  const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows), static_cast<unsigned>(runs < 65535 ? runs : 65535));
+  lookup_kernel<F, OutT, U><<<grid, kThreads, 0, stream>>>(a, lpr_log2, tvec, ovec);
   return cudaGetLastError();
+}
+
+// Small lookups spread over as many warps as there are (one piece per lane).
+template <Fmt F, typename OutT>
+cudaError_t launch_fmt(const LookupArgs& a, cudaStream_t stream) {
+  const double bytes = static_cast<double>(a.T) * static_cast<double>(a.D) * sizeof(OutT);
+  return bytes <= 4e6 ? launch_unroll<F, OutT, 1>(a, stream) : launch_unroll<F, OutT, 4>(a, stream);
 }
 
 template <Fmt F>
@@ -208,7 +245,9 @@ cudaError_t launch_out(const LookupArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t stream) {
+cudaError_t launch_lookup(const LookupArgs& args, cudaStream_t stream) {
+  LookupArgs a = args;
+  a.group_shift = a.w.group == 32 ? 5 : a.w.group == 64 ? 6 : 7;
   switch (a.fmt) {
     case BS_TABLE_BF16: return launch_out<Fmt::kBF16>(a, stream);
     case BS_TABLE_F32: return launch_out<Fmt::kF32>(a, stream);

@@ -41,7 +41,7 @@ struct Int4Matrix {
 
 cudaError_t launch_quantize_int4(const void* x, bool x_bf16, long long N, long long K, long long ldx, uint8_t* q,
                                  long long ldq, void* scale, bool scale_bf16, long long lds, uint8_t* zero,
-                                 long long ldz, int group, int sms, cudaStream_t stream);
+                                 long long ldz, int group, cudaStream_t stream);
 
 constexpr int kInt4MaxM = 32;  // activation rows of one product
 struct Int4Product {
@@ -77,6 +77,7 @@ struct LookupArgs {
   void* out;
   bool out_bf16;
   long long ldo;
+  int group_shift;  // filled in by launch_lookup
 };
 cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t stream);
 
