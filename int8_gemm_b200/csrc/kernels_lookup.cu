@@ -71,8 +71,8 @@ struct Piece {
     const uint8_t* p = row.data + (F == Fmt::kInt4 ? d / 2 : static_cast<long long>(d) * (kBytes / E));
     if constexpr (F == Fmt::kInt4) {
       const int g = d >> row.group_shift;
-      s = row.scale_bf16 ? __ldg(reinterpret_cast<const uint16_t*>(row.scale) + g)
-                         : __ldg(reinterpret_cast<const uint32_t*>(row.scale) + g);
+      s = row.scale_bf16 ? __ldg(reinterpret_cast<const uint16_t*>(row.scale + 2LL * g))
+                         : __ldg(reinterpret_cast<const uint32_t*>(row.scale + 4LL * g));
       z = row.zero ? __ldg(row.zero + g) : 8u;
     }
     if constexpr (F == Fmt::kE4M3) s = __ldg(reinterpret_cast<const uint32_t*>(row.scale) + (d >> 7));
@@ -126,9 +126,17 @@ struct Piece {
     } else if constexpr (F == Fmt::kInt4) {
       const float f = __uint_as_float(row.scale_bf16 ? s << 16 : s);
       // a nibble in the mantissa of 2^23 gives 2^23 + c; less 2^23 + z, exactly
-      const float off = __uint_as_float(0x4B000000u | (z & 15u));
+      const float off = -__uint_as_float(0x4B000000u | (z & 15u));
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = (__uint_as_float(0x4B000000u | ((w[0] >> (4 * i)) & 15u)) - off) * f;
+      for (int i = 0; i < E; i += 2) {
+        uint32_t lo, hi;  // (w >> 4 i) & 15 | 2^23 as one three-input operation after the shift
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(lo) : "r"(w[0] >> (4 * i)), "r"(15u), "r"(0x4B000000u));
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(hi) : "r"(w[0] >> (4 * i + 4)), "r"(15u), "r"(0x4B000000u));
+        const float2 c = __fadd2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(off, off));
+        const float2 x = __fmul2_rn(c, make_float2(f, f));
+        v[i] = x.x;
+        v[i + 1] = x.y;
+      }
     } else {
       const float f = F == Fmt::kE4M3 ? __uint_as_float(s) : e8m0_value(static_cast<uint8_t>(s));
 #pragma unroll
@@ -170,12 +178,45 @@ __device__ __forceinline__ void write_piece(OutT* p, const float (&v)[E], int le
   }
 }
 
+// U pieces of a row, the first at element d, E * lpr elements apart.  WHOLE: all
+// of them exist, on 16-byte boundaries, and lpr is 32 (so that their distances
+// are constants).
+template <Fmt F, typename OutT, int U, bool WHOLE>
+__device__ __forceinline__ void run_pieces(const LookupArgs& a, const Row<F>& row, bool named, int d, int lpr, int D,
+                                           bool tvec, bool ovec, OutT* out) {
+  constexpr int E = 16 / sizeof(OutT);
+  const int apart = WHOLE ? E * 32 : E * lpr;
+  Piece<F, E> piece[U];
+  if (named) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = d + u * apart;
+      if (WHOLE) piece[u].load(row, at, E, true);
+      else if (at < D) piece[u].load(row, at, D - at, tvec);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int at = d + u * apart;
+    if (!WHOLE && at >= D) break;
+    float v[E] = {};
+    if (named) {
+      piece[u].values(row, v);
+      if (a.alpha != 1.f) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= a.alpha;
+      }
+    }
+    write_piece<OutT, E>(out + at, v, WHOLE ? E : D - at, WHOLE || (ovec && D - at >= E));
+  }
+}
+
 // A warp's item: U pieces per lane of 32 / lpr rows, lpr lanes side by side in
 // a row.  blockIdx.x: kThreads / 32 items' rows; blockIdx.y: the run of U * lpr
 // pieces (gridDim.y runs apart).  tvec / ovec: table rows and output rows start
 // on 16-byte boundaries.
 template <Fmt F, typename OutT, int U>
-__global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a, int lpr_log2, bool tvec, bool ovec) {
+__global__ void __launch_bounds__(kThreads, 4) lookup_kernel(const LookupArgs a, int lpr_log2, bool tvec, bool ovec) {
   constexpr int E = 16 / sizeof(OutT);
   const int lane = threadIdx.x & 31, lpr = 1 << lpr_log2;
   const long long t = ((blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32) << (5 - lpr_log2)) + (lane >> lpr_log2);
@@ -188,25 +229,10 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a, in
   const int step = U * E * lpr;
   for (long long d0 = static_cast<long long>(blockIdx.y) * step; d0 < D; d0 += static_cast<long long>(gridDim.y) * step) {
     const int d = static_cast<int>(d0) + E * (lane & (lpr - 1));
-    Piece<F, E> piece[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = d + u * E * lpr;
-      if (named && at < D) piece[u].load(row, at, D - at, tvec);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = d + u * E * lpr;
-      if (at >= D) break;
-      float v[E] = {};
-      if (named) {
-        piece[u].values(row, v);
-        if (a.alpha != 1.f) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] *= a.alpha;
-        }
-      }
-      write_piece<OutT, E>(out + at, v, D - at, ovec && D - at >= E);
+    if (lpr_log2 == 5 && tvec && ovec && D - static_cast<int>(d0) >= step) {
+      run_pieces<F, OutT, U, true>(a, row, named, d, 32, D, true, true, out);
+    } else {
+      run_pieces<F, OutT, U, false>(a, row, named, d, lpr, D, tvec, ovec, out);
     }
   }
 }
@@ -235,7 +261,7 @@ cudaError_t launch_unroll(const LookupArgs& a, cudaStream_t stream) {
 template <Fmt F, typename OutT>
 cudaError_t launch_fmt(const LookupArgs& a, cudaStream_t stream) {
   const double bytes = static_cast<double>(a.T) * static_cast<double>(a.D) * sizeof(OutT);
-  return bytes <= 4e6 ? launch_unroll<F, OutT, 1>(a, stream) : launch_unroll<F, OutT, 4>(a, stream);
+  return bytes <= 4e6 ? launch_unroll<F, OutT, 1>(a, stream) : launch_unroll<F, OutT, F == Fmt::kBF16 || F == Fmt::kF32 ? 4 : 8>(a, stream);
 }
 
 template <Fmt F>
