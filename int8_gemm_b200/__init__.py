@@ -814,10 +814,10 @@ def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, a
     out = _rows_out(out, (V, D), out_dtype, index, device)
     h = lib()
     n = h.bs_embedding_grad_workspace(T, V, D)
-    ws = torch.empty(n, dtype=torch.uint8, device=device)  # the allocator's blocks are 512-byte aligned
+    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None  # the allocator's blocks are 512-byte aligned
     _launch(index, h.bs_embedding_grad, tok.data_ptr(), td, T, grad.data_ptr(), gd, ldg, V, D, float(alpha),
             -1 if padding_idx is None else int(padding_idx), out.data_ptr(), code, _unit_rows(out, "out"),
-            1 if accumulate else 0, ws.data_ptr(), n)
+            1 if accumulate else 0, None if ws is None else ws.data_ptr(), n)
     return out
 
 

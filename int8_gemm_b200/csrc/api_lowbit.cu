@@ -261,14 +261,15 @@ bs_status bs_embedding_grad(const void* tokens, bs_index_dtype token_dtype, int6
   bs_status st = check_rows_out(d, d_dtype, ldd, V, D);
   if (st != BS_OK) return st;
   if (T > 0) {
-    if (!tokens || !grad || !workspace) return api_fail(BS_ERR_NULL, "tokens, grad and workspace must be non-NULL");
+    const size_t need = lookup_grad_workspace(T, V, D);
+    if (!tokens || !grad || (need > 0 && !workspace))
+      return api_fail(BS_ERR_NULL, "tokens, grad and a workspace of that size must be non-NULL");
     if (!aligned(tokens, token_dtype == BS_INDEX_I64 ? 8 : 4))
       return api_fail(BS_ERR_ALIGNMENT, "tokens must be aligned to their size");
     if (ldg < D) return api_fail(BS_ERR_LAYOUT, "ldg=%lld < D=%lld", (long long)ldg, (long long)D);
     if (!extent_ok(T, ldg, 4)) return api_fail(BS_ERR_LAYOUT, "a stride times the number of rows is out of range");
     if (!aligned(grad, in_size(grad_dtype))) return api_fail(BS_ERR_ALIGNMENT, "grad must be aligned to its element size");
     if (!aligned(workspace, 256)) return api_fail(BS_ERR_ALIGNMENT, "the workspace must be 256-byte aligned");
-    const size_t need = lookup_grad_workspace(T, V, D);
     if (workspace_bytes < need)
       return api_fail(BS_ERR_WORKSPACE, "workspace of %zu bytes; this call needs %zu (bs_embedding_grad_workspace)",
                       workspace_bytes, need);

@@ -5,25 +5,32 @@
 // [0, V).  Sums are fp32 in an order that the tokens alone decide, rounded
 // once to the output type.
 //
-// Three launches.
+// Up to 1024 tokens, one launch (small_kernel): a CTA owns a range of table rows
+// and a slice of columns, reads every token, lists those of its rows in order,
+// zeroes the rows without one and sums the others' entries along links.
+//
+// More tokens, three launches.
 //   sort: one cluster of 8 CTAs sorts (token, position) pairs by token, stably,
-//     least significant 8-bit digit first (tokens that contribute nothing sort
-//     behind every row as key V).  Each warp owns a run of consecutive pairs
+//     by digits of up to 9 bits, the lowest first (tokens that contribute nothing
+//     sort behind every row as key V).  Each warp owns a run of consecutive pairs
 //     and counts its digits with match_any, the CTAs exchange their digit
 //     totals through distributed shared memory, and every pair's place follows
-//     from counts alone, so the order is the same on every run.
+//     from counts alone, so the order is the same on every run.  The other CTAs
+//     of the launch meanwhile zero the rows that no token names: each owns a
+//     range of rows and marks it from all tokens itself.
 //   rows: the sorted list in chunks of 32 pairs, whatever rows they belong to,
 //     so a row that many tokens name is spread over many CTAs.  A thread owns
 //     one 16-byte column piece and adds a row's pairs in list order.  Rows that
 //     begin and end inside a chunk are written; a row that crosses a chunk
-//     border leaves one partial sum per chunk in the workspace.  Further CTAs
-//     of the same launch zero the rows that no pair names.
+//     border leaves one partial sum per chunk in the workspace.
 //   join: the chunk in which a crossing row begins adds its partials in chunk
 //     order.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "lowbit.h"
+#include "quantize.h"
+#include "sm100.cuh"
 
 namespace bsg {
 
@@ -34,10 +41,12 @@ namespace cg = cooperative_groups;
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kDigits = 256;
-constexpr int kChunk = 32;     // sorted pairs per chunk
-constexpr int kZeroRows = 32;  // table rows per zeroing CTA
+constexpr int kMaxDigits = 512;
+constexpr int kSortSmem = kSortWarps * kMaxDigits * 4;
+constexpr int kChunk = 32;  // sorted pairs per chunk
 constexpr int kThreads = 256;
+constexpr int kSmallT = 1024;        // tokens that the single launch takes
+constexpr int kMarkRows = 16 * 8192;  // rows marked at a time: a 16 KB bitmap
 
 // Workspace: two (key, position) buffers of T pairs, then the partial sums of
 // each chunk's first and last row.
@@ -60,60 +69,107 @@ Layout layout_of(long long T, long long D) {
   return l;
 }
 
-// ---------------------------------------------------------------------------
-// sort
-// ---------------------------------------------------------------------------
-struct SortArgs {
+__device__ __forceinline__ float get(const float* p) { return *p; }
+__device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+struct Tokens {
   const void* tokens;
   bool tokens64;
   uint32_t T;
-  uint32_t V;  // also the key of pairs that contribute nothing
+  uint32_t V;  // also the key of tokens that contribute nothing
   long long padding_idx;
-  uint32_t *key[2], *pos[2];
-  int passes;  // pass i reads buffer i & 1 (pass 0: the tokens) and writes the other
+
+  __device__ __forceinline__ uint32_t key(uint32_t i) const {
+    const long long t = tokens64 ? __ldg(static_cast<const long long*>(tokens) + i) : __ldg(static_cast<const int*>(tokens) + i);
+    return t >= 0 && t < static_cast<long long>(V) && t != padding_idx ? static_cast<uint32_t>(t) : V;
+  }
 };
 
-__device__ __forceinline__ uint32_t token_key(const SortArgs& a, uint32_t i) {
-  const long long t = a.tokens64 ? static_cast<const long long*>(a.tokens)[i] : static_cast<const int*>(a.tokens)[i];
-  return t >= 0 && t < static_cast<long long>(a.V) && t != a.padding_idx ? static_cast<uint32_t>(t) : a.V;
+// Zeros in columns [d0, d1) of rows [v0, v1) whose bit is not set, a warp to a
+// row.  `vec`: rows start on 16-byte boundaries (and d0 is a whole piece).
+template <typename OutT>
+__device__ __forceinline__ void zero_rows(const uint32_t* named, long long v0, long long v1, OutT* out, long long ldo,
+                                          long long d0, long long d1, bool vec) {
+  constexpr int Z = 16 / sizeof(OutT);
+  const int warps = blockDim.x / 32, lane = threadIdx.x & 31;
+  for (long long v = v0 + threadIdx.x / 32; v < v1; v += warps) {
+    const uint32_t bit = static_cast<uint32_t>(v - v0);
+    if (named[bit / 32] >> (bit % 32) & 1u) continue;
+    OutT* p = out + v * ldo + d0;
+    const long long n = d1 - d0, whole = vec ? n / Z : 0;
+    for (long long i = lane; i < whole; i += 32) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = whole * Z + lane; i < n; i += 32) put(p + i, 0.f);
+  }
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a) {
-  __shared__ uint32_t hist[kSortWarps][kDigits];
-  __shared__ uint32_t total[kDigits];  // this CTA's digit counts, read by the whole cluster
-  __shared__ uint32_t base[kDigits];
-  __shared__ uint32_t warp_sum[kDigits / 32];
+// ---------------------------------------------------------------------------
+// sort, and the zeros beside it
+// ---------------------------------------------------------------------------
+struct SortArgs {
+  Tokens in;
+  uint32_t *key[2], *pos[2];
+  int passes, bits;  // pass i takes `bits` bits; reads buffer i & 1 (pass 0: the tokens) and writes the other
+  void* out;
+  long long ldo, D;
+  bool ovec;
+};
+
+// The pairs [lo, hi) of one warp, four rounds of 32 loaded at a time.
+template <typename Fn>
+__device__ __forceinline__ void each_pair(const SortArgs& a, int pass, uint32_t lo, uint32_t hi, Fn fn) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t* kin = a.key[pass & 1];
+  for (uint32_t i0 = lo; i0 < hi; i0 += 128) {
+    uint32_t k[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t i = i0 + 32 * r + lane;
+      k[r] = i >= hi ? 0u : (pass == 0 ? a.in.key(i) : kin[i]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t i = i0 + 32 * r + lane;
+      if (i0 + 32 * r < hi) fn(i, i < hi, k[r]);
+    }
+  }
+}
+
+__device__ __forceinline__ void sort_pairs(const SortArgs& a, uint32_t (*hist)[kMaxDigits]) {
+  __shared__ uint32_t total[kMaxDigits];  // this CTA's digit counts, read by the whole cluster
+  __shared__ uint32_t base[kMaxDigits];
+  __shared__ uint32_t warp_sum[kMaxDigits / 32];
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // this warp's pairs [lo, hi): runs of a multiple of 32, in (CTA, warp) order
-  const uint32_t runs = kSortCtas * kSortWarps;
-  const uint32_t per = ((a.T + runs - 1) / runs + 31) / 32 * 32;
+  const uint32_t runs = kSortCtas * kSortWarps, T = a.in.T;
+  const uint32_t per = (T / runs + 32) / 32 * 32;
   const uint64_t lo64 = static_cast<uint64_t>(rank * kSortWarps + warp) * per;
-  const uint32_t lo = lo64 < a.T ? static_cast<uint32_t>(lo64) : a.T;
-  const uint32_t hi = lo64 + per < a.T ? static_cast<uint32_t>(lo64 + per) : a.T;
+  const uint32_t lo = lo64 < T ? static_cast<uint32_t>(lo64) : T;
+  const uint32_t hi = lo64 + per < T ? static_cast<uint32_t>(lo64 + per) : T;
   const uint32_t below = (1u << lane) - 1u;
+  const int digits = 1 << a.bits;
+  const uint32_t mask = digits - 1;
 
   for (int pass = 0; pass < a.passes; ++pass) {
-    const int shift = 8 * pass;
-    const uint32_t* kin = a.key[pass & 1];
+    const int shift = a.bits * pass;
     const uint32_t* pin = a.pos[pass & 1];
     uint32_t* kout = a.key[(pass & 1) ^ 1];
     uint32_t* pout = a.pos[(pass & 1) ^ 1];
-    for (int d = lane; d < kDigits; d += 32) hist[warp][d] = 0;
+    for (int d = lane; d < digits; d += 32) hist[warp][d] = 0;
     __syncwarp();
-    for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint32_t k = !in ? 0u : (pass == 0 ? token_key(a, i) : kin[i]);
-      const uint32_t d = in ? (k >> shift) & 255u : kDigits;  // lanes past the end match one another only
+    each_pair(a, pass, lo, hi, [&](uint32_t, bool in, uint32_t k) {
+      const uint32_t d = in ? (k >> shift) & mask : kMaxDigits;  // lanes past the end match one another only
       const uint32_t same = __match_any_sync(0xffffffffu, d);
       if (in && (same & below) == 0) hist[warp][d] += __popc(same);
       __syncwarp();
-    }
+    });
     __syncthreads();
-    if (tid < kDigits) {  // counts of the warps before each warp, and the CTA's total
+    if (tid < digits) {  // counts of the warps before each warp, and the CTA's total
       uint32_t sum = 0;
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = hist[w][tid];
         hist[w][tid] = sum;
@@ -122,12 +178,15 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       total[tid] = sum;
     }
     cluster.sync();  // every CTA's totals are there
-    uint32_t before = 0, all = 0;
-    if (tid < kDigits) {
-      for (uint32_t r = 0; r < kSortCtas; ++r) {
-        const uint32_t c = *cluster.map_shared_rank(&total[tid], r);
-        before += r < rank ? c : 0u;
-        all += c;
+    if (tid < kMaxDigits) {
+      uint32_t before = 0, all = 0;
+      if (tid < digits) {
+#pragma unroll
+        for (uint32_t r = 0; r < kSortCtas; ++r) {
+          const uint32_t c = *cluster.map_shared_rank(&total[tid], r);
+          before += r < rank ? c : 0u;
+          all += c;
+        }
       }
       uint32_t incl = all;  // scan over the digits
       for (int o = 1; o < 32; o <<= 1) {
@@ -138,17 +197,14 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       base[tid] = incl - all + before;
     }
     __syncthreads();
-    if (tid < kDigits) {
+    if (tid < digits) {
       uint32_t pre = 0;
       for (int w = 0; w < warp; ++w) pre += warp_sum[w];
       base[tid] += pre;
     }
     __syncthreads();
-    for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint32_t k = !in ? 0u : (pass == 0 ? token_key(a, i) : kin[i]);
-      const uint32_t d = in ? (k >> shift) & 255u : kDigits;
+    each_pair(a, pass, lo, hi, [&](uint32_t i, bool in, uint32_t k) {
+      const uint32_t d = in ? (k >> shift) & mask : kMaxDigits;
       const uint32_t same = __match_any_sync(0xffffffffu, d);
       uint32_t at = 0;
       if (in) at = base[d] + hist[warp][d] + __popc(same & below);
@@ -159,10 +215,37 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         pout[at] = pass == 0 ? i : pin[i];
       }
       __syncwarp();
-    }
+    });
     // the pairs written here are read by other CTAs in the next pass, and this
     // CTA's totals are no longer read by any
     cluster.sync();
+  }
+}
+
+// Cluster 0 sorts; the CTAs of the others zero their share of the rows.
+template <typename OutT>
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_zero_kernel(const SortArgs a) {
+  extern __shared__ uint32_t sort_smem[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x < kSortCtas) {
+    sort_pairs(a, reinterpret_cast<uint32_t(*)[kMaxDigits]>(sort_smem));
+    return;
+  }
+  const long long share = blockIdx.x - kSortCtas, shares = gridDim.x - kSortCtas;
+  const long long v_lo = a.in.V * share / shares, v_hi = a.in.V * (share + 1) / shares;
+  for (long long v0 = v_lo; v0 < v_hi; v0 += kMarkRows) {
+    const uint32_t rows = static_cast<uint32_t>(v_hi - v0 < kMarkRows ? v_hi - v0 : kMarkRows);
+    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) sort_smem[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < a.in.T; i += kSortThreads) {
+      const uint32_t bit = a.in.key(i) - static_cast<uint32_t>(v0);  // wraps where the key is below v0
+      if (bit < rows) atomicOr(&sort_smem[bit / 32], 1u << (bit % 32));
+    }
+    __syncthreads();
+    zero_rows<OutT>(sort_smem, v0, v0 + rows, static_cast<OutT*>(a.out), a.ldo, 0, a.D, a.ovec);
+    __syncthreads();
   }
 }
 
@@ -180,7 +263,7 @@ struct RowArgs {
   bool accumulate;
   float* part;  // [chunks][2][dp]: a chunk's share of the row it begins in the middle of, and of the row it ends in
   long long dp;
-  uint32_t chunks, slices;  // column slices: gridDim.x = chunks * slices + zeroing CTAs
+  uint32_t chunks, slices;  // column slices: gridDim.x = chunks * slices
   bool gvec, ovec;
 };
 
@@ -210,11 +293,6 @@ __device__ __forceinline__ void load_piece(const InT* p, long long left, bool ve
     }
   }
 }
-
-__device__ __forceinline__ float get(const float* p) { return *p; }
-__device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // alpha * sum into E columns of a row (added to what is there when accumulating).
 template <typename OutT, int E>
@@ -247,83 +325,55 @@ template <typename InT, typename OutT>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs a) {
   constexpr int E = 16 / sizeof(InT);
   __shared__ uint32_t key[kChunk + 2], pos[kChunk];  // key[0] and key[kChunk + 1]: the neighbours'
-  const uint32_t work = a.chunks * a.slices;
-  if (blockIdx.x < work) {
-    const uint32_t c = blockIdx.x / a.slices, slice = blockIdx.x - c * a.slices;
-    const uint32_t i0 = c * kChunk;
-    for (int j = threadIdx.x; j < kChunk + 2; j += blockDim.x) {
-      const long long i = static_cast<long long>(i0) + j - 1;
-      key[j] = i >= 0 && i < a.T ? a.key[i] : a.V;  // a.V: no row
-      if (j < kChunk) pos[j] = i0 + j < a.T ? a.pos[i0 + j] : 0u;
-    }
-    __syncthreads();
-    const long long d = (static_cast<long long>(slice) * blockDim.x + threadIdx.x) * E;
-    if (d >= a.D) return;
-    const InT* g = static_cast<const InT*>(a.grad) + d;
-    float* part = a.part + static_cast<long long>(c) * 2 * a.dp + d;
-    float sum[E] = {};
-    bool from_before = key[0] == key[1];
-    for (int j0 = 0; j0 < kChunk; j0 += 4) {
-      float v[4][E];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (key[j0 + u + 1] < a.V) {
-          load_piece<InT>(g + pos[j0 + u] * a.ldg, a.D - d, a.gvec, v[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[u][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + u;
-        const uint32_t k = key[j + 1], next = key[j + 2];
-        if (k >= a.V) break;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] += v[u][e];
-        const bool last = j == kChunk - 1;
-        if (k != next || last) {
-          const bool crosses = from_before || (last && k == next);
-          if (crosses) {
-            float* p = part + (from_before ? 0 : a.dp);
-#pragma unroll
-            for (int e = 0; e < E; e += 4)
-              *reinterpret_cast<float4*>(p + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-          } else {
-            write_row<OutT, E>(a, k, d, sum);
-          }
-#pragma unroll
-          for (int e = 0; e < E; ++e) sum[e] = 0.f;
-          from_before = false;
-        }
-      }
-    }
-    return;
-  }
-  // zero the rows that no pair names
-  __shared__ bool named[kZeroRows];
-  const long long v0 = static_cast<long long>(blockIdx.x - work) * kZeroRows;
-  if (threadIdx.x < kZeroRows) {
-    const long long v = v0 + threadIdx.x;
-    uint32_t lo = 0, hi = a.T;  // the first key >= v
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (a.key[mid] < v) lo = mid + 1;
-      else hi = mid;
-    }
-    named[threadIdx.x] = v >= a.V || (lo < a.T && a.key[lo] == v);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t c = blockIdx.x / a.slices, slice = blockIdx.x - c * a.slices;
+  const uint32_t i0 = c * kChunk;
+  for (int j = threadIdx.x; j < kChunk + 2; j += blockDim.x) {
+    const long long i = static_cast<long long>(i0) + j - 1;
+    key[j] = i >= 0 && i < a.T ? a.key[i] : a.V;  // a.V: no row
+    if (j < kChunk) pos[j] = i0 + j < a.T ? a.pos[i0 + j] : 0u;
   }
   __syncthreads();
-  constexpr int Z = 16 / sizeof(OutT);
-  for (int r = 0; r < kZeroRows; ++r) {
-    if (named[r]) continue;
-    OutT* p = static_cast<OutT*>(a.out) + (v0 + r) * a.ldo;
-    if (a.ovec) {
-      const long long whole = a.D / Z;
-      for (long long i = threadIdx.x; i < whole; i += blockDim.x) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
-      for (long long i = whole * Z + threadIdx.x; i < a.D; i += blockDim.x) put(p + i, 0.f);
-    } else {
-      for (long long i = threadIdx.x; i < a.D; i += blockDim.x) put(p + i, 0.f);
+  const long long d = (static_cast<long long>(slice) * blockDim.x + threadIdx.x) * E;
+  if (d >= a.D) return;
+  const InT* g = static_cast<const InT*>(a.grad) + d;
+  float* part = a.part + static_cast<long long>(c) * 2 * a.dp + d;
+  float sum[E] = {};
+  bool from_before = key[0] == key[1];
+  for (int j0 = 0; j0 < kChunk; j0 += 4) {
+    float v[4][E];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (key[j0 + u + 1] < a.V) {
+        load_piece<InT>(g + pos[j0 + u] * a.ldg, a.D - d, a.gvec, v[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
+      const uint32_t k = key[j + 1], next = key[j + 2];
+      if (k >= a.V) break;
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += v[u][e];
+      const bool last = j == kChunk - 1;
+      if (k != next || last) {
+        const bool crosses = from_before || (last && k == next);
+        if (crosses) {
+          float* p = part + (from_before ? 0 : a.dp);
+#pragma unroll
+          for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4*>(p + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+        } else {
+          write_row<OutT, E>(a, k, d, sum);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = 0.f;
+        from_before = false;
+      }
     }
   }
 }
@@ -332,22 +382,139 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs a) {
 // chunk.
 template <typename OutT>
 __global__ void __launch_bounds__(kThreads) join_kernel(const RowArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const uint32_t c = blockIdx.x / a.slices, slice = blockIdx.x - c * a.slices;
   const long long first = static_cast<long long>(c) * kChunk, next = first + kChunk;
   if (next >= a.T) return;
-  const uint32_t k = a.key[next];
-  if (k >= a.V || a.key[next - 1] != k) return;                     // no row crosses this border
-  if (first > 0 && a.key[first] == k && a.key[first - 1] == k) return;  // it began in an earlier chunk
+  const uint32_t k = a.key[next], k_last = a.key[next - 1], k_first = a.key[first];
+  const uint32_t k_before = first > 0 ? a.key[first - 1] : a.V;
+  if (k >= a.V || k_last != k) return;              // no row crosses this border
+  if (k_first == k && k_before == k) return;        // it began in an earlier chunk
+  // chunks that it goes on through: those whose first key is its own
+  uint32_t more = 0;
+  for (long long i = next;; i += static_cast<long long>(blockDim.x) * kChunk) {
+    const long long at = i + static_cast<long long>(threadIdx.x) * kChunk;
+    const uint32_t n = __syncthreads_count(at < a.T && a.key[at] == k);
+    more += n;
+    if (n < blockDim.x) break;
+  }
   const long long d = (static_cast<long long>(slice) * blockDim.x + threadIdx.x) * 4;
   if (d >= a.D) return;
   float sum[4];
   const float4 h = *reinterpret_cast<const float4*>(a.part + (static_cast<long long>(c) * 2 + 1) * a.dp + d);
   sum[0] = h.x, sum[1] = h.y, sum[2] = h.z, sum[3] = h.w;
-  for (long long i = next; i < a.T && a.key[i] == k; i += kChunk) {
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (i / kChunk) * 2 * a.dp + d);
-    sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+  const float* p = a.part + (static_cast<long long>(c) + 1) * 2 * a.dp + d;
+  for (uint32_t i0 = 0; i0 < more; i0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u < more) v[u] = *reinterpret_cast<const float4*>(p + (static_cast<long long>(i0) + u) * 2 * a.dp);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u < more) sum[0] += v[u].x, sum[1] += v[u].y, sum[2] += v[u].z, sum[3] += v[u].w;
   }
   write_row<OutT, 4>(a, k, d, sum);
+}
+
+// ---------------------------------------------------------------------------
+// up to kSmallT tokens, in one launch
+// ---------------------------------------------------------------------------
+struct SmallArgs {
+  Tokens in;
+  RowArgs r;  // out, grad and their sizes; slices, gvec, ovec
+  uint32_t ranges;
+};
+
+template <typename InT, typename OutT>
+__global__ void __launch_bounds__(kThreads) small_kernel(const SmallArgs a) {
+  constexpr int E = 16 / sizeof(InT);
+  constexpr uint32_t kNone = 0xffffu;
+  __shared__ uint32_t named[kMarkRows / 32];
+  __shared__ uint32_t row[kSmallT];             // the listed tokens' rows, less v0
+  __shared__ uint16_t at[kSmallT], next[kSmallT];  // their positions, and the next entry of the same row
+  __shared__ uint8_t later[kSmallT];            // whether an earlier entry links to this one
+  __shared__ uint32_t warp_n[kThreads / 32 + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t range = blockIdx.x / a.r.slices, slice = blockIdx.x - range * a.r.slices;
+  const long long V = a.in.V;
+  const long long v_lo = V * range / a.ranges, v_hi = V * (range + 1) / a.ranges;
+  const long long width = static_cast<long long>(blockDim.x) * E;
+  const long long d0 = slice * width, d1 = d0 + width < a.r.D ? d0 + width : a.r.D;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (long long v0 = v_lo; v0 < v_hi; v0 += kMarkRows) {
+    const uint32_t rows = static_cast<uint32_t>(v_hi - v0 < kMarkRows ? v_hi - v0 : kMarkRows);
+    for (uint32_t i = tid; i < (rows + 31) / 32; i += blockDim.x) named[i] = 0;
+    __syncthreads();
+    uint32_t n = 0;  // entries listed so far
+    for (uint32_t i0 = 0; i0 < a.in.T; i0 += blockDim.x) {
+      const uint32_t i = i0 + tid;
+      const uint32_t bit = i < a.in.T ? a.in.key(i) - static_cast<uint32_t>(v0) : rows;  // wraps where below v0
+      const bool mine = bit < rows;
+      const uint32_t vote = __ballot_sync(0xffffffffu, mine);
+      if (lane == 0) warp_n[warp] = __popc(vote);
+      __syncthreads();
+      uint32_t before = n, all = n;
+      for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) {
+        if (w < warp) before += warp_n[w];
+        all += warp_n[w];
+      }
+      if (mine) {
+        const uint32_t e = before + __popc(vote & ((1u << lane) - 1u));
+        row[e] = bit;
+        at[e] = static_cast<uint16_t>(i);
+        next[e] = kNone;
+        later[e] = 0;
+        atomicOr(&named[bit / 32], 1u << (bit % 32));
+      }
+      n = all;
+      __syncthreads();
+    }
+    // link each entry to the next of its row
+    for (uint32_t e = tid; e < n; e += blockDim.x) {
+      const uint32_t mine = row[e];
+      for (uint32_t f = e + 1; f < n; ++f) {
+        if (row[f] == mine) {
+          next[e] = static_cast<uint16_t>(f);
+          later[f] = 1;
+          break;
+        }
+      }
+    }
+    if (!a.r.accumulate)
+      zero_rows<OutT>(named, v0, v0 + rows, static_cast<OutT*>(a.r.out), a.r.ldo, d0, d1, a.r.ovec);
+    __syncthreads();
+    const long long d = d0 + static_cast<long long>(tid) * E;
+    if (d < a.r.D) {
+      const InT* g = static_cast<const InT*>(a.r.grad) + d;
+      for (uint32_t h = 0; h < n; ++h) {
+        if (later[h]) continue;
+        float sum[E] = {};
+        uint32_t e = h;
+        while (e != kNone) {
+          float v[8][E];
+          int m = 0;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            if (e != kNone) {
+              load_piece<InT>(g + at[e] * a.r.ldg, a.r.D - d, a.r.gvec, v[u]);
+              e = next[e];
+              m = u + 1;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (u < m) {
+#pragma unroll
+              for (int x = 0; x < E; ++x) sum[x] += v[u][x];
+            }
+        }
+        write_row<OutT, E>(a.r, static_cast<uint32_t>(v0) + row[h], d, sum);
+      }
+    }
+    __syncthreads();
+  }
 }
 
 bool rows16(const void* base, long long ld_bytes) {
@@ -356,59 +523,30 @@ bool rows16(const void* base, long long ld_bytes) {
 
 int threads_for(long long pieces) { return pieces >= kThreads ? kThreads : static_cast<int>((pieces + 31) / 32 * 32); }
 
+// A launch that may begin while the previous kernel of the stream ends (every
+// kernel here waits for it before its first access).
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), long long grid, int threads, size_t smem, cudaStream_t stream,
+                         const Args& args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 template <typename InT, typename OutT>
-cudaError_t launch_rows(RowArgs r, cudaStream_t stream) {
+cudaError_t launch_types(const Tokens& in, const LookupGradArgs& a, int sms, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(InT);
-  r.gvec = rows16(r.grad, r.ldg * static_cast<long long>(sizeof(InT)));
-  r.ovec = rows16(r.out, r.ldo * static_cast<long long>(sizeof(OutT)));
-  const long long pieces = (r.D + E - 1) / E;
-  const int threads = threads_for(pieces);
-  r.slices = static_cast<uint32_t>((pieces + threads - 1) / threads);
-  const long long zero = r.accumulate ? 0 : (static_cast<long long>(r.V) + kZeroRows - 1) / kZeroRows;
-  const long long grid = static_cast<long long>(r.chunks) * r.slices + zero;
-  rows_kernel<InT, OutT><<<static_cast<unsigned>(grid), threads, 0, stream>>>(r);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || r.chunks < 2) return e;
-  const long long quads = (r.D + 3) / 4;
-  const int jt = threads_for(quads);
-  r.slices = static_cast<uint32_t>((quads + jt - 1) / jt);
-  join_kernel<OutT><<<static_cast<unsigned>((r.chunks - 1) * r.slices), jt, 0, stream>>>(r);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-size_t lookup_grad_workspace(long long T, long long V, long long D) {
-  (void)V;
-  return layout_of(T, D).bytes;
-}
-
-cudaError_t launch_lookup_grad(const LookupGradArgs& a, int sms, cudaStream_t stream) {
-  (void)sms;
-  const Layout l = layout_of(a.T, a.D);
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  SortArgs s;
-  s.tokens = a.tokens;
-  s.tokens64 = a.tokens64;
-  s.T = static_cast<uint32_t>(a.T);
-  s.V = static_cast<uint32_t>(a.V);
-  s.padding_idx = a.padding_idx;
-  for (int i = 0; i < 2; ++i) {
-    s.key[i] = reinterpret_cast<uint32_t*>(ws + l.key[i]);
-    s.pos[i] = reinterpret_cast<uint32_t*>(ws + l.pos[i]);
-  }
-  s.passes = 1;
-  while (s.passes < 4 && (static_cast<unsigned long long>(a.V) >> (8 * s.passes)) != 0) ++s.passes;
-  if (a.T > 0) {
-    sort_kernel<<<kSortCtas, kSortThreads, 0, stream>>>(s);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  RowArgs r;
-  r.key = s.key[s.passes & 1];
-  r.pos = s.pos[s.passes & 1];
-  r.T = s.T;
-  r.V = s.V;
+  RowArgs r = {};
+  r.T = in.T;
+  r.V = in.V;
   r.grad = a.grad;
   r.ldg = a.ldg;
   r.D = a.D;
@@ -416,13 +554,78 @@ cudaError_t launch_lookup_grad(const LookupGradArgs& a, int sms, cudaStream_t st
   r.out = a.out;
   r.ldo = a.ldo;
   r.accumulate = a.accumulate;
+  r.gvec = rows16(a.grad, a.ldg * static_cast<long long>(sizeof(InT)));
+  r.ovec = rows16(a.out, a.ldo * static_cast<long long>(sizeof(OutT)));
+  const long long pieces = (a.D + E - 1) / E;
+  const int threads = threads_for(pieces);
+  r.slices = static_cast<uint32_t>((pieces + threads - 1) / threads);
+
+  if (a.T <= kSmallT) {
+    SmallArgs s;
+    s.in = in;
+    s.r = r;
+    // ranges of rows for about four CTAs per SM
+    const long long want = (4LL * sms + r.slices - 1) / r.slices;
+    s.ranges = static_cast<uint32_t>(want < a.V ? want : a.V);
+    return launch_after(small_kernel<InT, OutT>, static_cast<long long>(s.ranges) * r.slices, threads, 0, stream, s);
+  }
+
+  const Layout l = layout_of(a.T, a.D);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  SortArgs s;
+  s.in = in;
+  for (int i = 0; i < 2; ++i) {
+    s.key[i] = reinterpret_cast<uint32_t*>(ws + l.key[i]);
+    s.pos[i] = reinterpret_cast<uint32_t*>(ws + l.pos[i]);
+  }
+  int total_bits = 1;  // of the largest key, V
+  while (total_bits < 32 && (static_cast<unsigned long long>(a.V) >> total_bits) != 0) ++total_bits;
+  s.passes = (total_bits + 8) / 9;
+  s.bits = (total_bits + s.passes - 1) / s.passes;
+  s.out = a.out;
+  s.ldo = a.ldo;
+  s.D = a.D;
+  s.ovec = r.ovec;
+  int per_sm = 0;
+  cudaError_t e = ctas_per_sm_once<sort_zero_kernel<OutT>>(kSortThreads, kSortSmem, &per_sm);
+  if (e != cudaSuccess) return e;
+  // beside the sort, zeroing clusters for two CTAs on every SM
+  const long long clusters = a.accumulate ? 1 : (2LL * sms + kSortCtas - 1) / kSortCtas;
+  e = launch_after(sort_zero_kernel<OutT>, clusters * kSortCtas, kSortThreads, kSortSmem, stream, s);
+  if (e != cudaSuccess) return e;
+
+  r.key = s.key[s.passes & 1];
+  r.pos = s.pos[s.passes & 1];
   r.part = reinterpret_cast<float*>(ws + l.part);
   r.dp = l.dp;
   r.chunks = static_cast<uint32_t>(l.chunks);
+  e = launch_after(rows_kernel<InT, OutT>, static_cast<long long>(r.chunks) * r.slices, threads, 0, stream, r);
+  if (e != cudaSuccess) return e;
+  const long long quads = (a.D + 3) / 4;
+  const int jt = threads_for(quads);
+  r.slices = static_cast<uint32_t>((quads + jt - 1) / jt);
+  return launch_after(join_kernel<OutT>, (static_cast<long long>(r.chunks) - 1) * r.slices, jt, 0, stream, r);
+}
+
+}  // namespace
+
+size_t lookup_grad_workspace(long long T, long long V, long long D) {
+  (void)V;
+  return T <= kSmallT ? 0 : layout_of(T, D).bytes;
+}
+
+cudaError_t launch_lookup_grad(const LookupGradArgs& a, int sms, cudaStream_t stream) {
+  Tokens in;
+  in.tokens = a.tokens;
+  in.tokens64 = a.tokens64;
+  in.T = static_cast<uint32_t>(a.T);
+  in.V = static_cast<uint32_t>(a.V);
+  in.padding_idx = a.padding_idx;
   if (a.T == 0 && a.accumulate) return cudaSuccess;
   if (a.grad_bf16)
-    return a.out_bf16 ? launch_rows<__nv_bfloat16, __nv_bfloat16>(r, stream) : launch_rows<__nv_bfloat16, float>(r, stream);
-  return a.out_bf16 ? launch_rows<float, __nv_bfloat16>(r, stream) : launch_rows<float, float>(r, stream);
+    return a.out_bf16 ? launch_types<__nv_bfloat16, __nv_bfloat16>(in, a, sms, stream)
+                      : launch_types<__nv_bfloat16, float>(in, a, sms, stream);
+  return a.out_bf16 ? launch_types<float, __nv_bfloat16>(in, a, sms, stream) : launch_types<float, float>(in, a, sms, stream);
 }
 
 }  // namespace bsg

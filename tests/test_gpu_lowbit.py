@@ -396,7 +396,9 @@ def _grad_check(tokens, grad, V, alpha=1.0, padding_idx=None, out_dtype=F, grad_
 
 @pytest.mark.parametrize("grad_dtype,out_dtype", [(BF, F), (F, F), (BF, BF), (F, BF)])
 @pytest.mark.parametrize("T,V,D", [(1, 1, 1), (31, 10, 7), (32, 10, 8), (33, 3, 64), (64, 1, 100), (65, 40, 33), (255, 7168, 101),
-                                   (1000, 256, 264), (4096, 255, 16), (5000, 70000, 40), (513, 20, 2056)])
+                                   (1000, 256, 264), (4096, 255, 16), (5000, 70000, 40), (513, 20, 2056),
+                                   (1024, 300, 130), (1025, 300, 130), (1024, 1, 20), (1025, 1, 20), (1500, 511, 9),
+                                   (1500, 512, 2050), (20000, 300000, 4)])
 def test_gradient(T, V, D, grad_dtype, out_dtype):
     g = _gen(T + V + D)
     # the frequencies of text, and tokens outside the table among them
@@ -409,7 +411,7 @@ def test_gradient(T, V, D, grad_dtype, out_dtype):
     _grad_check(tokens, grad, V, 0.25, 0, out_dtype, base=torch.randn(V, D, generator=g).to(out_dtype).to(DEV))
 
 
-@pytest.mark.parametrize("T", [1, 31, 32, 33, 63, 64, 65, 96, 97, 8192, 20000])
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 63, 64, 65, 96, 97, 1023, 1024, 1025, 1056, 1057, 8192, 20000])
 def test_gradient_one_row_takes_all(T):
     """A single row named by every token, at the ends of the table and among others."""
     D, V = 24, 1000
@@ -524,11 +526,27 @@ def test_offsets_past_32_bits():
     assert int(torch.count_nonzero(d[1:V - 3].view(-1)[:2**30])) == 0 and int(torch.count_nonzero(d[V - 1000:V - 3])) == 0
 
 
+@pytest.mark.slow
+@pytest.mark.parametrize("T", [1000, 5000])
+def test_gradient_of_a_very_long_table(T):
+    """More rows than a CTA marks at a time; small integers, so that every sum is exact."""
+    V, D = 90_000_001, 2
+    g = _gen(T)
+    tokens = torch.randint(0, V, (T,), generator=g)
+    tokens[::7] = V - 1
+    tokens[1::7] = 0
+    grad = torch.randint(-8, 9, (T, D), generator=g).float()
+    d = torch.full((V, D), 5.0, device=DEV)
+    bs.bs_embedding_grad(tokens.to(DEV), grad.to(DEV), V, out=d)
+    want = torch.zeros(V, D, device=DEV).index_add_(0, tokens.to(DEV), grad.to(DEV))
+    assert torch.equal(d, want)
+
+
 def test_other_stream_and_threads():
     host, dev = _matrix(300, 512, 64, 21)
     x = torch.randn(4, 512, generator=_gen(1)).to(DEV)
-    tokens = torch.randint(0, 300, (500,), generator=_gen(2)).to(DEV)
-    grad = torch.randn(500, 64, generator=_gen(3)).to(DEV)
+    tokens = torch.randint(0, 300, (5000,), generator=_gen(2)).to(DEV)
+    grad = torch.randn(5000, 64, generator=_gen(3)).to(DEV)
     want = (bs.bs_gemv_int4(x, *dev, group=64, out_dtype=F), bs.bs_embedding_grad(tokens, grad, 300))
     torch.cuda.synchronize()
     errors = []
@@ -552,7 +570,7 @@ def test_other_stream_and_threads():
 
 def test_captured_graphs_replayed_on_new_inputs():
     """Two graphs of all five operators, captured one after the other and replayed in turn on inputs that change."""
-    V, D, T, group = 64, 128, 96, 32
+    V, D, T, group = 64, 128, 1200, 32
     w = torch.randn(V, D, generator=_gen(1)).to(DEV)
     tokens = [torch.randint(0, V, (T,), generator=_gen(i)).to(DEV) for i in (2, 3)]
 

@@ -125,10 +125,10 @@ def test_embedding_refusals():
 
 
 def _grad(**kw):
-    a = dict(tok=P, td=1, T=70, grad=P, gd=0, ldg=300, V=50, D=300, alpha=1.0, pad=-1, d=P, od=1, ldd=300, acc=0, ws=P,
+    a = dict(tok=P, td=1, T=2000, grad=P, gd=0, ldg=300, V=50, D=300, alpha=1.0, pad=-1, d=P, od=1, ldd=300, acc=0, ws=P,
              n=None)
     a.update(kw)
-    n = bs.lib().bs_embedding_grad_workspace(70, 50, 300) if a["n"] is None else a["n"]
+    n = bs.lib().bs_embedding_grad_workspace(2000, 50, 300) if a["n"] is None else a["n"]
     return bs.lib().bs_embedding_grad(v(a["tok"]), a["td"], a["T"], v(a["grad"]), a["gd"], a["ldg"], a["V"], a["D"],
                                       a["alpha"], a["pad"], v(a["d"]), a["od"], a["ldd"], a["acc"], v(a["ws"]), n, None)
 
@@ -146,12 +146,14 @@ def test_embedding_grad_refusals():
     assert _grad(V=0) == bs.BS_OK and _grad(D=0) == bs.BS_OK
     if not HAS_GPU:
         assert _grad() == bs.BS_ERR_DEVICE and _grad(T=0, tok=0, grad=0, ws=0, n=0) == bs.BS_ERR_DEVICE
+        assert _grad(T=1024, ws=0, n=0) == bs.BS_ERR_DEVICE
 
 
 def test_embedding_grad_workspace_covers_pairs_and_partials():
     size = bs.lib().bs_embedding_grad_workspace
     assert size(0, 100, 64) == 0 and size(-1, 5, 5) == 0 and size(5, 1 << 31, 5) == 0
-    for T, D in ((1, 1), (33, 7), (16640, 5120)):
+    assert size(1, 100, 64) == 0 and size(1024, 100, 64) == 0  # few tokens need none
+    for T, D in ((1025, 1), (1100, 7), (16640, 5120)):
         assert size(T, 1000, D) >= 16 * T + 2 * -(-T // 32) * 4 * D
         assert size(T, 1000, D) == size(T, 5, D)
     assert size(2**31 - 1, 2**31 - 1, 2**31 - 1) > 2**58
