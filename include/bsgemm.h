@@ -451,7 +451,7 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
  *   grad     bf16 or fp32 [T, D], row stride ldg (>= D)
  *   d        [V, D], row stride ldd (>= D), BS_OUT_BF16 or BS_OUT_F32
  *   workspace  bs_embedding_grad_workspace(T, V, D) bytes, 256-byte aligned (0
- *            bytes, and NULL, for up to 1024 tokens);
+ *            bytes, and NULL, for up to 512 tokens);
  *            its contents need not be set and mean nothing afterwards.  Calls
  *            that overlap on the GPU need a workspace each.
  * T and V are below 2^31, D below 2^30.  Pointers are aligned to their element sizes (rows

@@ -5,24 +5,26 @@
 // [0, V).  Sums are fp32 in an order that the tokens alone decide, rounded
 // once to the output type.
 //
-// Up to 1024 tokens, one launch (small_kernel): a CTA owns a range of table rows
+// Up to kSmallT tokens, one launch (small_kernel): a CTA owns a range of table rows
 // and a slice of columns, reads every token, lists those of its rows in order,
 // zeroes the rows without one and sums the others' entries along links.
 //
 // More tokens, three launches.
-//   sort: one cluster of 8 CTAs sorts (token, position) pairs by token, stably,
-//     by digits of up to 9 bits, the lowest first (tokens that contribute nothing
-//     sort behind every row as key V).  Each warp owns a run of consecutive pairs
-//     and counts its digits with match_any, the CTAs exchange their digit
-//     totals through distributed shared memory, and every pair's place follows
-//     from counts alone, so the order is the same on every run.  The other CTAs
-//     of the launch meanwhile zero the rows that no token names: each owns a
-//     range of rows and marks it from all tokens itself.
+//   sort: (token, position) pairs by token, stably; tokens that contribute nothing
+//     sort behind every row as key V.  Up to kRankMaxT tokens each pair's place
+//     is counted by comparing it with all others (rank_kernel: T^2 comparisons on
+//     all SMs, no hand-over between them).  Beyond, one cluster of 8 CTAs sorts
+//     by digits of up to 9 bits, the lowest first: each warp owns a run of
+//     consecutive pairs and counts its digits with match_any, the CTAs exchange
+//     their digit totals through distributed shared memory, and every pair's
+//     place follows from counts alone.  Either way the order is the same on
+//     every run.
 //   rows: the sorted list in chunks of 32 pairs, whatever rows they belong to,
 //     so a row that many tokens name is spread over many CTAs.  A thread owns
 //     one 16-byte column piece and adds a row's pairs in list order.  Rows that
 //     begin and end inside a chunk are written; a row that crosses a chunk
-//     border leaves one partial sum per chunk in the workspace.
+//     border leaves one partial sum per chunk in the workspace.  Further CTAs
+//     of the launch zero the rows that no pair names.
 //   join: the chunk in which a crossing row begins adds its partials in chunk
 //     order.
 #include <cooperative_groups.h>
@@ -45,7 +47,10 @@ constexpr int kMaxDigits = 512;
 constexpr int kSortSmem = kSortWarps * kMaxDigits * 4;
 constexpr int kChunk = 32;  // sorted pairs per chunk
 constexpr int kThreads = 256;
-constexpr int kSmallT = 1024;        // tokens that the single launch takes
+constexpr int kZeroRows = 32;  // rows per zeroing CTA of rows_kernel
+constexpr int kSmallT = 512;         // tokens that the single launch takes (D = 512: 200 tokens 16 us, 1000 tokens 31 us against 21)
+constexpr int kRankTokens = 32, kRankWays = kThreads / kRankTokens;  // per CTA of rank_kernel; threads per token
+constexpr long long kRankMaxT = 4096;  // tokens up to which it is the faster sort (whole gradient, D = 512: 27 us against 30; 8192: 36 against 35)
 constexpr int kMarkRows = 16 * 8192;  // rows marked at a time: a 16 KB bitmap
 
 // Workspace: two (key, position) buffers of T pairs, then the partial sums of
@@ -87,33 +92,34 @@ struct Tokens {
   }
 };
 
-// Zeros in columns [d0, d1) of rows [v0, v1) whose bit is not set, a warp to a
-// row.  `vec`: rows start on 16-byte boundaries (and d0 is a whole piece).
+// Zeros in columns [d0, d1) of rows [v0, v1) whose bit is not set, as many
+// threads side by side in a row as it has pieces (so that long rows are written
+// as one run).  `vec`: rows start on 16-byte boundaries (and d0 is a whole piece).
 template <typename OutT>
 __device__ __forceinline__ void zero_rows(const uint32_t* named, long long v0, long long v1, OutT* out, long long ldo,
                                           long long d0, long long d1, bool vec) {
   constexpr int Z = 16 / sizeof(OutT);
-  const int warps = blockDim.x / 32, lane = threadIdx.x & 31;
-  for (long long v = v0 + threadIdx.x / 32; v < v1; v += warps) {
+  const long long n = d1 - d0, whole = vec ? n / Z : 0;
+  int log2 = 5;  // threads per row
+  while ((2 << log2) <= static_cast<int>(blockDim.x) && (1 << log2) < (vec ? whole : n)) ++log2;
+  const int side = 1 << log2, t = threadIdx.x & (side - 1), rows = blockDim.x >> log2;
+  if (static_cast<int>(threadIdx.x >> log2) >= rows) return;  // a block that is no power of two
+  for (long long v = v0 + (threadIdx.x >> log2); v < v1; v += rows) {
     const uint32_t bit = static_cast<uint32_t>(v - v0);
     if (named[bit / 32] >> (bit % 32) & 1u) continue;
     OutT* p = out + v * ldo + d0;
-    const long long n = d1 - d0, whole = vec ? n / Z : 0;
-    for (long long i = lane; i < whole; i += 32) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
-    for (long long i = whole * Z + lane; i < n; i += 32) put(p + i, 0.f);
+    for (long long i = t; i < whole; i += side) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = whole * Z + t; i < n; i += side) put(p + i, 0.f);
   }
 }
 
 // ---------------------------------------------------------------------------
-// sort, and the zeros beside it
+// sort
 // ---------------------------------------------------------------------------
 struct SortArgs {
   Tokens in;
   uint32_t *key[2], *pos[2];
   int passes, bits;  // pass i takes `bits` bits; reads buffer i & 1 (pass 0: the tokens) and writes the other
-  void* out;
-  long long ldo, D;
-  bool ovec;
 };
 
 // The pairs [lo, hi) of one warp, four rounds of 32 loaded at a time.
@@ -222,30 +228,75 @@ __device__ __forceinline__ void sort_pairs(const SortArgs& a, uint32_t (*hist)[k
   }
 }
 
-// Cluster 0 sorts; the CTAs of the others zero their share of the rows.
-template <typename OutT>
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_zero_kernel(const SortArgs a) {
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a) {
   extern __shared__ uint32_t sort_smem[];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (blockIdx.x < kSortCtas) {
-    sort_pairs(a, reinterpret_cast<uint32_t(*)[kMaxDigits]>(sort_smem));
-    return;
-  }
-  const long long share = blockIdx.x - kSortCtas, shares = gridDim.x - kSortCtas;
-  const long long v_lo = a.in.V * share / shares, v_hi = a.in.V * (share + 1) / shares;
-  for (long long v0 = v_lo; v0 < v_hi; v0 += kMarkRows) {
-    const uint32_t rows = static_cast<uint32_t>(v_hi - v0 < kMarkRows ? v_hi - v0 : kMarkRows);
-    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) sort_smem[i] = 0;
+  sort_pairs(a, reinterpret_cast<uint32_t(*)[kMaxDigits]>(sort_smem));
+}
+
+// A CTA places kRankTokens pairs: a pair's place is the number of pairs before
+// it, counted over all tokens by kRankWays threads per pair.  Keys are below
+// 2^24 and compared as fp32 integers: the saturated difference bound - k is 1
+// where k < bound and 0 elsewhere, one full-rate operation where an integer
+// comparison and its count take three of half rate.
+__global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
+  constexpr int kTile = 2048, kLoads = kTile / kThreads, kPart = kTile / kRankWays;
+  __shared__ float4 tile[kTile / 4];
+  __shared__ float counts[kRankWays][kRankTokens];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  float* flat = reinterpret_cast<float*>(tile);
+  const uint32_t T = a.in.T, i0 = blockIdx.x * kRankTokens;
+  const int slot = threadIdx.x % kRankTokens, way = threadIdx.x / kRankTokens;
+  const uint32_t i = i0 + slot;
+  const uint32_t key = i < T ? a.in.key(i) : a.in.V;
+  const float fkey = static_cast<float>(key);
+  float count = 0.f;  // at most T
+  float next[kLoads];  // the next tile's keys
+  auto fetch = [&](uint32_t j0) {
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r) {
+      const uint32_t j = j0 + r * kThreads + threadIdx.x;
+      next[r] = j < T ? static_cast<float>(a.in.key(j)) : 3e38f;  // before no pair
+    }
+  };
+  fetch(0);
+  for (uint32_t j0 = 0; j0 < T; j0 += kTile) {
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r) flat[r * kThreads + threadIdx.x] = next[r];
     __syncthreads();
-#pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < a.in.T; i += kSortThreads) {
-      const uint32_t bit = a.in.key(i) - static_cast<uint32_t>(v0);  // wraps where the key is below v0
-      if (bit < rows) atomicOr(&sort_smem[bit / 32], 1u << (bit % 32));
+    if (j0 + kTile < T) fetch(j0 + kTile);
+    const float4* mine = tile + way * (kPart / 4);
+    if (j0 + kTile <= i0 || j0 >= i0 + kRankTokens) {
+      // equal keys come before where their position does
+      const float bound = j0 < i0 ? fkey + 1.f : fkey;
+      float c[4] = {};
+#pragma unroll 8
+      for (int q = 0; q < kPart / 4; ++q) {
+        const float4 k = mine[q];
+        c[0] += __saturatef(bound - k.x);
+        c[1] += __saturatef(bound - k.y);
+        c[2] += __saturatef(bound - k.z);
+        c[3] += __saturatef(bound - k.w);
+      }
+      count += (c[0] + c[1]) + (c[2] + c[3]);
+    } else {
+      for (int q = 0; q < kPart; ++q) {
+        const uint32_t j = j0 + way * kPart + q;
+        count += __saturatef((j < i ? fkey + 1.f : fkey) - flat[way * kPart + q]);
+      }
     }
     __syncthreads();
-    zero_rows<OutT>(sort_smem, v0, v0 + rows, static_cast<OutT*>(a.out), a.ldo, 0, a.D, a.ovec);
-    __syncthreads();
+  }
+  counts[way][slot] = count;
+  __syncthreads();
+  if (way == 0 && i < T) {
+#pragma unroll
+    for (int w = 1; w < kRankWays; ++w) count += counts[w][slot];
+    const uint32_t at = static_cast<uint32_t>(count);
+    a.key[0][at] = key;
+    a.pos[0][at] = i;
   }
 }
 
@@ -263,36 +314,46 @@ struct RowArgs {
   bool accumulate;
   float* part;  // [chunks][2][dp]: a chunk's share of the row it begins in the middle of, and of the row it ends in
   long long dp;
-  uint32_t chunks, slices;  // column slices: gridDim.x = chunks * slices
+  uint32_t chunks, slices;  // of columns
   bool gvec, ovec;
 };
 
+// 16 bytes of a gradient row, as read.
 template <typename InT>
-__device__ __forceinline__ void load_piece(const InT* p, long long left, bool vec, float (&v)[16 / sizeof(InT)]) {
-  constexpr int E = 16 / sizeof(InT);
-  if (vec && left >= E) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Piece {
+  static constexpr int E = 16 / sizeof(InT);
+  uint32_t w[4];
+
+  // `left` of its elements exist (the others are zero); `vec`: rows start on
+  // 16-byte boundaries.
+  __device__ __forceinline__ void load(const InT* p, long long left, bool vec) {
+    if (vec && left >= E) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (i >= left) continue;
+      if constexpr (E == 4) w[i] = __float_as_uint(p[i]);
+      else w[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[i])) << (16 * (i % 2));
+    }
+  }
+
+  __device__ __forceinline__ void add_to(float (&sum)[E]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (E == 4) {
-        v[i] = __uint_as_float(w[i]);
+        sum[i] += __uint_as_float(w[i]);
       } else {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      v[i] = 0.f;
-      if (i < left) {
-        if constexpr (E == 4) v[i] = p[i];
-        else v[i] = __bfloat162float(p[i]);
+        sum[2 * i] += __uint_as_float(w[i] << 16);
+        sum[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
       }
     }
   }
-}
+};
 
 // alpha * sum into E columns of a row (added to what is there when accumulating).
 template <typename OutT, int E>
@@ -321,12 +382,34 @@ __device__ __forceinline__ void write_row(const RowArgs& a, uint32_t v, long lon
     if (i < left) put(p + i, a.accumulate ? __fadd_rn(get(p + i), y[i]) : y[i]);
 }
 
+// gridDim.x: the chunks' slices, then CTAs that zero kZeroRows rows each (mixed
+// evenly among the chunks they cost the gradient of 16640 tokens on a table of
+// 131072 x 5120 504 us in place of 450).
 template <typename InT, typename OutT>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs a) {
   constexpr int E = 16 / sizeof(InT);
   __shared__ uint32_t key[kChunk + 2], pos[kChunk];  // key[0] and key[kChunk + 1]: the neighbours'
   grid_dependency_wait();
   grid_launch_dependents();
+  const uint32_t work = a.chunks * a.slices;
+  if (blockIdx.x >= work) {  // zeros: the rows that no pair names
+    const long long v0 = static_cast<long long>(blockIdx.x - work) * kZeroRows;
+    const long long v1 = v0 + kZeroRows < a.V ? v0 + kZeroRows : a.V;
+    if (threadIdx.x < 32) {
+      const long long v = v0 + threadIdx.x;
+      uint32_t lo = 0, hi = a.T;  // the first key >= v
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (a.key[mid] < v) lo = mid + 1;
+        else hi = mid;
+      }
+      const uint32_t bits = __ballot_sync(0xffffffffu, lo < a.T && a.key[lo] == v);
+      if (threadIdx.x == 0) key[0] = bits;
+    }
+    __syncthreads();
+    zero_rows<OutT>(key, v0, v1, static_cast<OutT*>(a.out), a.ldo, 0, a.D, a.ovec);
+    return;
+  }
   const uint32_t c = blockIdx.x / a.slices, slice = blockIdx.x - c * a.slices;
   const uint32_t i0 = c * kChunk;
   for (int j = threadIdx.x; j < kChunk + 2; j += blockDim.x) {
@@ -341,24 +424,18 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowArgs a) {
   float* part = a.part + static_cast<long long>(c) * 2 * a.dp + d;
   float sum[E] = {};
   bool from_before = key[0] == key[1];
+#pragma unroll 1
   for (int j0 = 0; j0 < kChunk; j0 += 4) {
-    float v[4][E];
+    Piece<InT> v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (key[j0 + u + 1] < a.V) {
-        load_piece<InT>(g + pos[j0 + u] * a.ldg, a.D - d, a.gvec, v[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[u][e] = 0.f;
-      }
-    }
+    for (int u = 0; u < 4; ++u)
+      if (key[j0 + u + 1] < a.V) v[u].load(g + pos[j0 + u] * a.ldg, a.D - d, a.gvec);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = j0 + u;
       const uint32_t k = key[j + 1], next = key[j + 2];
       if (k >= a.V) break;
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum[e] += v[u][e];
+      v[u].add_to(sum);
       const bool last = j == kChunk - 1;
       if (k != next || last) {
         const bool crosses = from_before || (last && k == next);
@@ -493,22 +570,19 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const SmallArgs a) {
         float sum[E] = {};
         uint32_t e = h;
         while (e != kNone) {
-          float v[8][E];
+          Piece<InT> v[8];
           int m = 0;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             if (e != kNone) {
-              load_piece<InT>(g + at[e] * a.r.ldg, a.r.D - d, a.r.gvec, v[u]);
+              v[u].load(g + at[e] * a.r.ldg, a.r.D - d, a.r.gvec);
               e = next[e];
               m = u + 1;
             }
           }
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            if (u < m) {
-#pragma unroll
-              for (int x = 0; x < E; ++x) sum[x] += v[u][x];
-            }
+            if (u < m) v[u].add_to(sum);
         }
         write_row<OutT, E>(a.r, static_cast<uint32_t>(v0) + row[h], d, sum);
       }
@@ -578,20 +652,20 @@ cudaError_t launch_types(const Tokens& in, const LookupGradArgs& a, int sms, cud
     s.key[i] = reinterpret_cast<uint32_t*>(ws + l.key[i]);
     s.pos[i] = reinterpret_cast<uint32_t*>(ws + l.pos[i]);
   }
-  int total_bits = 1;  // of the largest key, V
-  while (total_bits < 32 && (static_cast<unsigned long long>(a.V) >> total_bits) != 0) ++total_bits;
-  s.passes = (total_bits + 8) / 9;
-  s.bits = (total_bits + s.passes - 1) / s.passes;
-  s.out = a.out;
-  s.ldo = a.ldo;
-  s.D = a.D;
-  s.ovec = r.ovec;
-  int per_sm = 0;
-  cudaError_t e = ctas_per_sm_once<sort_zero_kernel<OutT>>(kSortThreads, kSortSmem, &per_sm);
-  if (e != cudaSuccess) return e;
-  // beside the sort, zeroing clusters for two CTAs on every SM
-  const long long clusters = a.accumulate ? 1 : (2LL * sms + kSortCtas - 1) / kSortCtas;
-  e = launch_after(sort_zero_kernel<OutT>, clusters * kSortCtas, kSortThreads, kSortSmem, stream, s);
+  cudaError_t e;
+  if (a.T <= kRankMaxT && a.V < (1 << 24)) {
+    s.passes = s.bits = 0;
+    e = launch_after(rank_kernel, (a.T + kRankTokens - 1) / kRankTokens, kThreads, 0, stream, s);
+  } else {
+    int total_bits = 1;  // of the largest key, V
+    while (total_bits < 32 && (static_cast<unsigned long long>(a.V) >> total_bits) != 0) ++total_bits;
+    s.passes = (total_bits + 8) / 9;
+    s.bits = (total_bits + s.passes - 1) / s.passes;
+    int per_sm = 0;
+    e = ctas_per_sm_once<sort_kernel>(kSortThreads, kSortSmem, &per_sm);
+    if (e != cudaSuccess) return e;
+    e = launch_after(sort_kernel, kSortCtas, kSortThreads, kSortSmem, stream, s);
+  }
   if (e != cudaSuccess) return e;
 
   r.key = s.key[s.passes & 1];
@@ -599,7 +673,8 @@ cudaError_t launch_types(const Tokens& in, const LookupGradArgs& a, int sms, cud
   r.part = reinterpret_cast<float*>(ws + l.part);
   r.dp = l.dp;
   r.chunks = static_cast<uint32_t>(l.chunks);
-  e = launch_after(rows_kernel<InT, OutT>, static_cast<long long>(r.chunks) * r.slices, threads, 0, stream, r);
+  const long long zeros = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
+  e = launch_after(rows_kernel<InT, OutT>, static_cast<long long>(r.chunks) * r.slices + zeros, threads, 0, stream, r);
   if (e != cudaSuccess) return e;
   const long long quads = (a.D + 3) / 4;
   const int jt = threads_for(quads);

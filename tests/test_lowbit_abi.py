@@ -146,14 +146,14 @@ def test_embedding_grad_refusals():
     assert _grad(V=0) == bs.BS_OK and _grad(D=0) == bs.BS_OK
     if not HAS_GPU:
         assert _grad() == bs.BS_ERR_DEVICE and _grad(T=0, tok=0, grad=0, ws=0, n=0) == bs.BS_ERR_DEVICE
-        assert _grad(T=1024, ws=0, n=0) == bs.BS_ERR_DEVICE
+        assert _grad(T=512, ws=0, n=0) == bs.BS_ERR_DEVICE
 
 
 def test_embedding_grad_workspace_covers_pairs_and_partials():
     size = bs.lib().bs_embedding_grad_workspace
     assert size(0, 100, 64) == 0 and size(-1, 5, 5) == 0 and size(5, 1 << 31, 5) == 0
-    assert size(1, 100, 64) == 0 and size(1024, 100, 64) == 0  # few tokens need none
-    for T, D in ((1025, 1), (1100, 7), (16640, 5120)):
+    assert size(1, 100, 64) == 0 and size(512, 100, 64) == 0  # few tokens need none
+    for T, D in ((513, 1), (1100, 7), (16640, 5120)):
         assert size(T, 1000, D) >= 16 * T + 2 * -(-T // 32) * 4 * D
         assert size(T, 1000, D) == size(T, 5, D)
     assert size(2**31 - 1, 2**31 - 1, 2**31 - 1) > 2**58
