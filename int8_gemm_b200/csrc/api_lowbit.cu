@@ -130,7 +130,7 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
   if (M > kInt4MaxM)
     return api_fail(BS_ERR_SHAPE, "M=%lld: at most %d rows (bs_dequantize_int4 and a GEMM serve more)", (long long)M,
                     kInt4MaxM);
-  if (N > kMaxDim || K > (kMaxDim >> 1)) return api_fail(BS_ERR_SHAPE, "N exceeds 2^31-1 or K 2^30-1");
+  if (N > (kMaxDim >> 1) || K > (kMaxDim >> 1)) return api_fail(BS_ERR_SHAPE, "size exceeds 2^30-1");
   if (!in_known(x_dtype)) return api_fail(BS_ERR_DTYPE, "x must be bf16 or f32");
   if (!out_known(out_dtype)) return api_fail(BS_ERR_DTYPE, "bs_gemv_int4 writes bf16 or f32 only");
   bs_status st = check_int4(q, ldq, scale, scale_dtype, ld_scale, zero, ld_zero, group, N, K);
@@ -166,10 +166,7 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
   p.M = static_cast<int>(M);
   p.N = N;
   p.K = K;
-  CUtensorMap map;
-  st = api_map_codes(&map, q, (K + 1) / 2, N, ldq, kInt4TileBytes, kInt4TileRows, CU_TENSOR_MAP_SWIZZLE_64B);
-  if (st != BS_OK) return st;
-  return api_launched(launch_gemv_int4(p, map, sms, err, cs), "4-bit product launch");
+  return api_launched(launch_gemv_int4(p, sms, err, cs), "4-bit product launch");
 }
 
 bs_status bs_embedding(const void* tokens, bs_index_dtype token_dtype, int64_t T, const void* table, bs_table_fmt format,

@@ -9,21 +9,26 @@
 // no weight is ever rounded.  fp32 activations are split into three bf16
 // parts that add up to them exactly, one MMA each.
 //
-// A CTA owns 256 matrix rows and a run of 128-deep K blocks, which pass
-// through a ring of stages in shared memory.  One thread fetches a block's
-// codes (256 rows x 64 bytes) with a tensor copy; four staging warps write its
-// activations in the order of the MMA's fragments (fp32 split on the way) and
-// its scales and zero points as (scale, 128 + z) pairs; eight warps multiply,
-// 32 rows each, so that a fragment of activations serves two 16-row tiles.
+// Eight warps share a CTA's tile of matrix rows, KW of them splitting K; each
+// works alone until its sums meet the others' in shared memory (added in warp
+// order).  A warp keeps a ring of its own tensor copies in flight, 16 RT rows x
+// 64 bytes (128 k) each, and runs ahead into the CTA's next tile; persistent
+// CTAs take every gridDim.x-th tile.  For a 128-deep block it holds the
+// activations of 128 k as MMA fragments and passes its RT 16-row tiles by them.
 // In a block a thread takes, for rows g and g + 8 of a tile (g = lane / 4), the
 // word of 8 codes at k = 32 u + 8 (lane % 4) for u = 0 .. 3: all lanes' word u
 // lies in the same 32 k, so every MMA sums inside one group whatever the group
 // size, and under the copy's 64-byte swizzle (16-byte piece c of row r at
 // c ^ (r / 2 % 4)) the lanes' words fall on different banks.  A word's nibbles
 // j and j + 4 form the MMA's k pairs, and the activations are paired the same
-// way.  With few row tiles K is split over the CTAs of a cluster, whose partial
-// tiles meet in distributed shared memory and are added in rank order.
-#include <cooperative_groups.h>
+// way.  The four lanes of a row load four consecutive groups' scales and zero
+// points at once, one span of blocks ahead, and pass them round by shuffles.
+//
+// What bounds it: not memory but the issue of a warp's dependent instructions.
+// A word of 8 codes costs 11 operations to unpack (3 shifts, 4 three-input
+// logical, 4 bf16 subtractions, all at half rate), NT MMAs of 8 pipe cycles and
+// about 8 more for activations, scales, sums and the ring.  131072 x 5120, groups
+// of 128, bf16: one row 86 us, 16 rows 125, where the copies alone take 52.
 #include <cuda_bf16.h>
 
 #include "lowbit.h"
@@ -34,20 +39,10 @@ namespace bsg {
 
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kMmaWarps = 8;    // 32 rows each
-constexpr int kFillWarps = 3;   // staging activations and scales; one warp more issues the tensor copies
-constexpr int kThreads = 32 * (kMmaWarps + 1 + kFillWarps);
-constexpr int kTiles = 2;  // 16-row tiles per warp
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kUnits = 4;  // 32-k units per block
-constexpr int kCodeBytes = kInt4TileRows * kInt4TileBytes;
-constexpr int kScaleGroups = 4;  // groups of a slot of scales: 4, 2 or 1 blocks
-constexpr int kScalePitch = kInt4TileRows * 8 + 64;  // bytes between a slot's groups (64: a load's groups store to different banks)
-constexpr int kScaleBytes = kScaleGroups * kScalePitch;
-constexpr int kScaleStages = 3;
-constexpr int kPitch = kInt4TileRows + 4;  // floats between the rows of a partial tile
-static_assert(kMmaWarps * kTiles * 16 == kInt4TileRows && kUnits * 16 == kInt4TileBytes, "tile and box agree");
+static_assert(kUnits * 16 == kInt4BoxBytes, "block and box agree");
 
 // d = a b + (first ? 0 : d)
 __device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -131,325 +126,313 @@ struct Eight {
   }
 };
 
-// GPB: groups per 128-deep block (1, 2 or 4); NT: tiles of 8 activation rows.
-template <typename XT, int GPB, int NT>
+// GPB: groups per 128-deep block (1, 2 or 4); NT: tiles of 8 activation rows;
+// RT: 16-row tiles of the matrix per warp; ZERO: the matrix has zero points.
+// The ring is as deep as leaves room for kCtas CTAs on an SM (a third stage that
+// cost the second CTA: 128 us in place of 101 on 131072 x 5120, one row).
+template <typename XT, int NT, int RT>
 struct Config {
   static constexpr int kParts = sizeof(XT) == 2 ? 1 : 3;
-  static constexpr int kXBytes = kUnits * NT * kParts * 512;  // fragments: 16 bytes per lane
-  static constexpr int kStageBytes = kCodeBytes + kXBytes;
-  static constexpr int kCtas = NT <= 2 && sizeof(XT) == 2 ? 2 : 1;  // per SM
-  static constexpr int kRoom = 225 * 1024 / kCtas - kScaleStages * kScaleBytes - 2048;
-  static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
-  static constexpr int kSmem = kStages * kStageBytes + kScaleStages * kScaleBytes + 1024;  // 1024: the first stage's alignment
-  static_assert(kStages >= 3, "a ring");
-  static_assert(kStages * kStageBytes >= 8 * NT * kPitch * 4, "the partial tile takes the ring's place");
+  static constexpr int kCtas = NT * kParts == 1 && RT == 1 ? 3 : (NT * kParts <= 2 ? 2 : 1);  // per SM
+  static constexpr int kBoxBytes = 16 * RT * kInt4BoxBytes;
+  static constexpr int kStages = RT == 4 ? 2 : (RT == 2 ? 3 : 4);
+  static constexpr int kPitch = 16 * RT + 4;  // floats between the activation rows of a warp's sums
+  static constexpr int kRingBytes = kWarps * kStages * kBoxBytes;
+  static constexpr int kSmem = kRingBytes + kWarps * 8 * NT * kPitch * 4 + 1024;  // 1024: the first box's alignment
 };
 
-// Grid: S consecutive CTAs (a cluster) per row tile, splitting its K blocks.
-template <typename XT, int GPB, int NT>
-__global__ void __launch_bounds__(kThreads, Config<XT, GPB, NT>::kCtas)
-    gemv_int4_kernel(const __grid_constant__ CUtensorMap tmq, const Int4Product p, int S, bool xvec, uint32_t* err) {
-  using C = Config<XT, GPB, NT>;
-  constexpr int PARTS = C::kParts;
-  constexpr int kSpan = kScaleGroups / GPB;  // blocks per scale slot
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::kStages], empty[C::kStages], sfull[kScaleStages], sempty[kScaleStages];
-  __shared__ int abort_flag;
-  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* scales = ring + C::kStages * C::kStageBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
-  const int rank = static_cast<int>(blockIdx.x) % S;
-  const long long n0 = static_cast<long long>(blockIdx.x / S) * kInt4TileRows;
-  const int KB = static_cast<int>((p.K + 127) / 128);
-  const int kb_lo = static_cast<int>(static_cast<long long>(KB) * rank / S);
-  const int blocks = static_cast<int>(static_cast<long long>(KB) * (rank + 1) / S) - kb_lo;
+// Scales (raw bits) or zero points of a lane's 2 RT rows for one of four
+// consecutive groups.
+template <int RT>
+struct Side {
+  uint32_t s[2 * RT], z[2 * RT];
+};
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 2);  // the tensor copy's arrival and the activations'
-      mbar_init(&empty[s], kMmaWarps);
+template <typename XT, int GPB, int NT, int RT, bool ZERO>
+__global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
+    gemv_int4_kernel(const __grid_constant__ CUtensorMap tmq, const Int4Product p, int kw, uint32_t tiles, bool xvec,
+                     uint32_t* err) {
+  using C = Config<XT, NT, RT>;
+  constexpr int PARTS = C::kParts;
+  constexpr int kSpan = 4 / GPB;  // blocks that a load of scales serves
+  constexpr int kUnitsPerGroup = kUnits / GPB;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kWarps][C::kStages];
+  __shared__ int abort_flag;
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* sums = reinterpret_cast<float*>(base + C::kRingBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
+  uint8_t* ring = base + warp * C::kStages * C::kBoxBytes;
+  // this warp's K blocks [kb_lo, kb_lo + nb) and its rows within a tile
+  const int KB = static_cast<int>((p.K + 127) / 128);
+  const int part_k = warp & (kw - 1), row0 = 16 * RT * (warp / kw);
+  const int kb_lo = static_cast<int>(static_cast<long long>(KB) * part_k / kw);
+  const int nb = static_cast<int>(static_cast<long long>(KB) * (part_k + 1) / kw) - kb_lo;
+  const int tile_rows = 16 * RT * (kWarps / kw);
+
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(&full[warp][s], 1);
+    if (warp == 0) {
+      abort_flag = 0;
+      tma_prefetch_desc(&tmq);
     }
-    for (int s = 0; s < kScaleStages; ++s) {
-      mbar_init(&sfull[s], 1);
-      mbar_init(&sempty[s], kMmaWarps);
-    }
-    abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmq);
   }
   __syncthreads();
   grid_dependency_wait();  // every operand may come from the previous kernel in the stream
   grid_launch_dependents();
 
-  float acc[kTiles][NT][4] = {};
-  if (warp < kMmaWarps) {
-    constexpr int kUnitsPerGroup = kUnits / GPB;
-    uint32_t word_off[kUnits];  // word u of row gr of the warp's first tile
+  // the next box to copy, and the stage it goes to
+  uint32_t copy_tile = blockIdx.x;
+  int copy_b = 0, copy_st = 0;
+  auto copy = [&]() {
+    if (copy_tile < tiles && nb > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[warp][copy_st], C::kBoxBytes);
+        tma_load_3d(ring + copy_st * C::kBoxBytes, &tmq, &full[warp][copy_st], (kb_lo + copy_b) * kInt4BoxBytes,
+                    static_cast<int>(copy_tile) * tile_rows + row0, 0);
+      }
+      if (++copy_st == C::kStages) copy_st = 0;
+      if (++copy_b == nb) copy_b = 0, copy_tile += gridDim.x;
+    }
+  };
+  for (int s = 0; s < C::kStages; ++s) copy();
+
+  const int K = static_cast<int>(p.K), G = static_cast<int>((p.K + p.w.group - 1) / p.w.group);
+  const XT* xrow[NT];
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u)
-      word_off[u] = (32 * warp + gr) * kInt4TileBytes + 4 * t + ((u ^ ((gr >> 1) & 3)) << 4);
-    int st = 0, sst = 0, in_slot = 0;
-    uint32_t phase = 0, sphase = 0;
-    for (int b = 0; b < blocks; ++b) {
-      if (in_slot == 0 &&
-          !wait_bounded(&sfull[sst], sphase, &abort_flag, err, kErrTimeout | kRoleConsumer | kWaitScaleFull))
-        break;
-      if (!wait_bounded(&full[st], phase, &abort_flag, err, kErrTimeout | kRoleConsumer | kWaitStageFull)) break;
-      const uint8_t* stage = ring + st * C::kStageBytes;
-      const uint4* xs = reinterpret_cast<const uint4*>(stage + kCodeBytes) + lane;
-      const uint2* sc = reinterpret_cast<const uint2*>(scales + sst * kScaleBytes + in_slot * GPB * kScalePitch) + 32 * warp + gr;
-      uint2 so[kTiles][2];  // (scale, 128 + z) of rows gr and gr + 8 of each tile
-      float part[kTiles][NT][4];
+  for (int j = 0; j < NT; ++j) xrow[j] = static_cast<const XT*>(p.x) + (8 * j + gr < p.M ? 8 * j + gr : 0) * p.ldx + 8 * t;
+  // scales and zero points of the span that begins with block kb of `tile`
+  const int scale_bytes = p.w.scale_bf16 ? 2 : 4;
+  const long long step_s = 8 * p.w.lds * scale_bytes, step_z = 8 * p.w.ldz;
+  const char* scale_g = static_cast<const char*>(p.w.scale) + t * scale_bytes;
+  auto load_side = [&](Side<RT>& f, uint32_t tile, int kb) {
+    const int n = static_cast<int>(tile) * tile_rows + row0 + gr;
+    // rows left from n, none where the group or the tile does not exist
+    const int left = tile < tiles && kb * GPB + t < G ? static_cast<int>(p.N) - n : 0;
+    const char* sp = scale_g + (n * p.w.lds + kb * GPB) * scale_bytes;
+    if (p.w.scale_bf16) {
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const bool first = u % kUnitsPerGroup == 0, last = u % kUnitsPerGroup == kUnitsPerGroup - 1;
-        uint32_t a[kTiles][2][4];
+      for (int i = 0; i < 2 * RT; ++i, sp += step_s) f.s[i] = left > 8 * i ? __ldg(reinterpret_cast<const uint16_t*>(sp)) : 0u;
+    } else {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
+      for (int i = 0; i < 2 * RT; ++i, sp += step_s) f.s[i] = left > 8 * i ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : 0u;
+    }
+    if constexpr (ZERO) {
+      const uint8_t* zp = p.w.zero + n * p.w.ldz + kb * GPB + t;
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i, zp += step_z) f.z[i] = left > 8 * i ? __ldg(zp) : 8u;
+    }
+  };
+  uint32_t word_off[kUnits];  // word u of row gr of a 16-row tile
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) word_off[u] = gr * kInt4BoxBytes + 4 * t + ((u ^ ((gr >> 1) & 3)) << 4);
+
+  Side<RT> now, next;
+  if (nb > 0) load_side(next, blockIdx.x, kb_lo);
+  const uint32_t scale_shift = p.w.scale_bf16 ? 16 : 0;
+  int st = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+#pragma unroll 1
+    for (int b = 0; b < nb; ++b) {
+      const int slot = (b % kSpan) * GPB;  // of this block's first group among the four loaded
+      if (slot == 0) {
+        now = next;
+        if (b + kSpan < nb) load_side(next, tile, kb_lo + b + kSpan);
+        else load_side(next, tile + gridDim.x, kb_lo);
+      }
+      // the block's activations
+      uint4 x[kUnits][NT][PARTS];
+      {
+        const int k0 = (kb_lo + b) * 128;
+        if (xvec && k0 + 128 <= K) {
+          Eight<XT> v[kUnits][NT];
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) v[u][j].load16(xrow[j] + k0 + 32 * u, 8 * j + gr < p.M);
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) v[u][j].template pairs<PARTS>(x[u][j]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              Eight<XT> v;
+              v.load(xrow[j] + k0 + 32 * u, 8 * j + gr < p.M ? K - k0 - 32 * u - 8 * t : 0);
+              v.template pairs<PARTS>(x[u][j]);
+            }
+        }
+      }
+      if (ok) ok = wait_bounded(&full[warp][st], phase, &abort_flag, err, kErrTimeout | kRoleConsumer | kWaitStageFull);
+      if (!ok) break;
+      const uint8_t* box = ring + st * C::kBoxBytes;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float part[NT][4];
+        uint32_t off0 = 0x43084308u, off1 = 0x43084308u;  // 128 + z, twice: one unit of the last place of bf16's 128 is 1
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          const bool first = u % kUnitsPerGroup == 0, last = u % kUnitsPerGroup == kUnitsPerGroup - 1;
           if (first) {
-            so[i][0] = sc[(u / kUnitsPerGroup) * (kScalePitch / 8) + 16 * i];
-            so[i][1] = sc[(u / kUnitsPerGroup) * (kScalePitch / 8) + 16 * i + 8];
+            const int src = (lane & ~3) | (slot + u / kUnitsPerGroup);
+            s0 = __uint_as_float(__shfl_sync(0xffffffffu, now.s[2 * i], src) << scale_shift);
+            s1 = __uint_as_float(__shfl_sync(0xffffffffu, now.s[2 * i + 1], src) << scale_shift);
+            if constexpr (ZERO) {
+              off0 = ((__shfl_sync(0xffffffffu, now.z[2 * i], src) & 15u) | 0x4300u) * 0x10001u;
+              off1 = ((__shfl_sync(0xffffffffu, now.z[2 * i + 1], src) & 15u) | 0x4300u) * 0x10001u;
+            }
           }
-          const uint8_t* c = stage + word_off[u] + 16 * i * kInt4TileBytes;
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(c);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(c + 8 * kInt4TileBytes);
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(box + word_off[u] + 16 * i * kInt4BoxBytes);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(box + word_off[u] + (16 * i + 8) * kInt4BoxBytes);
+          uint32_t a[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            a[i][h][0] = code_pair(w0, 2 * h, so[i][0].y);
-            a[i][h][1] = code_pair(w1, 2 * h, so[i][1].y);
-            a[i][h][2] = code_pair(w0, 2 * h + 1, so[i][0].y);
-            a[i][h][3] = code_pair(w1, 2 * h + 1, so[i][1].y);
+            a[h][0] = code_pair(w0, 2 * h, off0);
+            a[h][1] = code_pair(w1, 2 * h, off1);
+            a[h][2] = code_pair(w0, 2 * h + 1, off0);
+            a[h][3] = code_pair(w1, 2 * h + 1, off1);
           }
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
 #pragma unroll
           for (int c = PARTS - 1; c >= 0; --c) {  // the smallest parts first
-            const uint4 x = xs[((u * NT + j) * PARTS + c) * 32];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) mma_bf16_16x8x16(part[i][j], a[i][0], x.x, x.y, first && c == PARTS - 1);
+            for (int j = 0; j < NT; ++j) mma_bf16_16x8x16(part[j], a[0], x[u][j][c].x, x[u][j][c].y, first && c == PARTS - 1);
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) mma_bf16_16x8x16(part[i][j], a[i][1], x.z, x.w, false);
+            for (int j = 0; j < NT; ++j) mma_bf16_16x8x16(part[j], a[1], x[u][j][c].z, x[u][j][c].w, false);
           }
-        }
-        if (last) {
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
+          if (last) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(__uint_as_float(so[i][e / 2].x), part[i][j][e], acc[i][j][e]);
+              for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(e < 2 ? s0 : s1, part[j][e], acc[i][j][e]);
+          }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
       if (++st == C::kStages) st = 0, phase ^= 1;
-      if (++in_slot == kSpan) {
-        if (lane == 0) mbar_arrive(&sempty[sst]);
-        in_slot = 0;
-        if (++sst == kScaleStages) sst = 0, sphase ^= 1;
-      }
+      __syncwarp();  // every lane has read the box
+      copy();
     }
-  } else if (warp == kMmaWarps) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t phase = 1;  // of the stage's previous use
-      for (int b = 0; b < blocks; ++b) {
-        if (b >= C::kStages &&
-            !wait_bounded(&empty[st], phase, &abort_flag, err, kErrTimeout | kRoleProducer | kWaitStageEmpty))
-          break;
-        mbar_arrive_expect_tx(&full[st], kCodeBytes);
-        tma_load_3d(ring + st * C::kStageBytes, &tmq, &full[st], (kb_lo + b) * kInt4TileBytes, static_cast<int>(n0), 0);
-        if (++st == C::kStages) st = 0, phase ^= 1;
-      }
-      // a wait that gave up leaves copies in flight: let them land before the CTA retires
-      if (abort_flag) pause_ns(1000000);
-    }
-  } else {
-    // block b's activations are warp b % 3's, and so are the scales of slot s;
-    // each warp takes its tasks in the order of the blocks they belong to
-    const int a = warp - kMmaWarps - 1;
-    const int K = static_cast<int>(p.K), G = static_cast<int>((p.K + p.w.group - 1) / p.w.group);
-    const XT* xrow[NT];
+    // the warps' sums [activation row][matrix row], added in order of K
+    float* mine = sums + warp * 8 * NT * C::kPitch;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xrow[j] = static_cast<const XT*>(p.x) + (8 * j + gr < p.M ? 8 * j + gr : 0) * p.ldx;
-    const int col = lane % kScaleGroups, row = lane / kScaleGroups;  // 4 groups of 8 rows per load
-    for (int b = 0; b < blocks; ++b) {
-      if (b % kSpan == 0 && (b / kSpan) % kFillWarps == a) {
-        const int slot = b / kSpan, sst = slot % kScaleStages;
-        const int g = (kb_lo + b) * GPB + col;
-        uint8_t* dst = scales + sst * kScaleBytes + col * kScalePitch + row * 8;
-        bool waited = slot < kScaleStages;
-#pragma unroll 1
-        for (int r0 = 0; r0 < kInt4TileRows; r0 += 128) {
-          // all loads first (a conversion beside its load would wait for it)
-          uint32_t sv[16], zv[16];
-          const long long n = n0 + r0 + row;
-          const bool g_in = g < G;
-          if (p.w.scale_bf16) {
-            const uint16_t* sp = static_cast<const uint16_t*>(p.w.scale) + n * p.w.lds + g;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sv[i] = g_in && n + 8 * i < p.N ? __ldg(sp + 8 * i * p.w.lds) : 0u;
-          } else {
-            const uint32_t* sp = static_cast<const uint32_t*>(p.w.scale) + n * p.w.lds + g;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sv[i] = g_in && n + 8 * i < p.N ? __ldg(sp + 8 * i * p.w.lds) : 0u;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) zv[i] = 8;
-          if (p.w.zero) {
-            const uint8_t* zp = p.w.zero + n * p.w.ldz + g;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) zv[i] = g_in && n + 8 * i < p.N ? __ldg(zp + 8 * i * p.w.ldz) : 8u;
-          }
-          if (!waited) {
-            waited = wait_bounded(&sempty[sst], (slot / kScaleStages - 1) & 1u, &abort_flag, err,
-                                  kErrTimeout | kRoleScale | kWaitScaleEmpty);
-            if (!waited) break;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)  // one unit of the last place of bf16's 128 is 1
-            *reinterpret_cast<uint2*>(dst + (r0 + 8 * i) * 8) = make_uint2(p.w.scale_bf16 ? sv[i] << 16 : sv[i], (0x4300u + (zv[i] & 15u)) * 0x10001u);
-        }
-        if (!waited) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[sst]);
-      }
-      if (b % kFillWarps != a) continue;
-      const int st = b % C::kStages;
-      const int k0 = (kb_lo + b) * 128 + 8 * t;
-      uint4* xs = reinterpret_cast<uint4*>(ring + st * C::kStageBytes + kCodeBytes) + lane;
-      const bool whole = xvec && (kb_lo + b) * 128 + 128 <= K;
-      bool waited = b < C::kStages;
-      constexpr int kAhead = NT * sizeof(XT) <= 8 ? kUnits : 2;  // units whose loads are in flight together
-#pragma unroll 1
-      for (int u0 = 0; u0 < kUnits; u0 += kAhead) {
-        Eight<XT> v[kAhead][NT];
-        if (whole) {
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) v[u][j].load16(xrow[j] + k0 + 32 * (u0 + u), 8 * j + gr < p.M);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const int k = k0 + 32 * (u0 + u);
-              v[u][j].load(xrow[j] + k, 8 * j + gr < p.M ? K - k : 0);
-            }
-        }
-        if (!waited) {
-          waited = wait_bounded(&empty[st], (b / C::kStages - 1) & 1u, &abort_flag, err,
-                                kErrTimeout | kRoleProducer | kWaitStageEmpty);
-          if (!waited) break;
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint4 x[PARTS];
-            v[u][j].template pairs<PARTS>(x);
-#pragma unroll
-            for (int c = 0; c < PARTS; ++c) xs[(((u0 + u) * NT + j) * PARTS + c) * 32] = x[c];
-          }
-      }
-      if (!waited) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[st]);
-    }
-  }
-
-  // the warps' sums as a partial tile [activation row][matrix row], over the ring
-  __syncthreads();
-  float* tile = reinterpret_cast<float*>(ring);
-  if (warp < kMmaWarps) {
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          tile[(8 * j + 2 * t + e % 2) * kPitch + 32 * warp + 16 * i + 8 * (e / 2) + gr] = acc[i][j][e];
-  }
-  cg::cluster_group cluster = cg::this_cluster();
-  if (S > 1) cluster.sync();
-  else __syncthreads();
-  // CTA `rank` finishes its share of the activation rows
-  for (int i = threadIdx.x; i < p.M * kInt4TileRows; i += kThreads) {
-    const int m = i / kInt4TileRows, r = i % kInt4TileRows;
-    if (m % S != rank || n0 + r >= p.N) continue;
-    float y = 0.f;
-    if (S > 1) {
-      for (int c = 0; c < S; ++c) y += *cluster.map_shared_rank(tile + m * kPitch + r, c);
-    } else {
-      y = tile[m * kPitch + r];
+          mine[(8 * j + 2 * t + e % 2) * C::kPitch + 16 * i + 8 * (e / 2) + gr] = acc[i][j][e];
+    __syncthreads();
+    // kThreads is a multiple of the tile's rows, so a thread keeps its row
+    const int r = threadIdx.x & (tile_rows - 1);
+    const long long n = static_cast<long long>(tile) * tile_rows + r;
+    if (n < p.N) {
+      const float bias = p.bias ? p.bias[n] : 0.f;
+      const int m_step = kThreads / tile_rows;
+      int m = threadIdx.x / tile_rows;
+      const float* from = sums + ((r / (16 * RT)) * kw * 8 * NT + m) * C::kPitch + (r & (16 * RT - 1));
+      for (; m < p.M; m += m_step, from += m_step * C::kPitch) {
+        float y = from[0];
+        for (int w = 1; w < kw; ++w) y += from[w * 8 * NT * C::kPitch];
+        y += bias;
+        const long long o = m * p.ldo + n;
+        if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+        else static_cast<float*>(p.out)[o] = y;
+      }
     }
-    if (p.bias) y += p.bias[n0 + r];
-    const long long o = m * p.ldo + n0 + r;
-    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
-    else static_cast<float*>(p.out)[o] = y;
+    __syncthreads();
   }
-  if (S > 1) cluster.sync();  // a CTA's tile stays until every rank has read it
+  // a wait that gave up leaves copies in flight: let them land before the CTA retires
+  if (!ok) pause_ns(1000000);
 }
 
-// K splits of a row tile (a power of two up to 8) on a GPU that holds `slots`
-// CTAs: the one with the least K blocks on the busiest slot, counting a CTA's
-// fixed costs as two blocks.
-int splits_for(long long tiles, long long blocks, long long slots) {
-  int best = 1;
-  long long least = 0;
-  for (int S = 1; S <= 8 && S <= blocks; S *= 2) {
-    const long long cost = ((tiles * S + slots - 1) / slots) * ((blocks + S - 1) / S + 2);
-    if (S == 1 || cost < least) best = S, least = cost;
-  }
-  return best;
-}
-
-template <typename XT, int GPB, int NT>
-cudaError_t launch_one(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
-  using C = Config<XT, GPB, NT>;
+template <typename XT, int GPB, int NT, int RT, bool ZERO>
+cudaError_t launch_zero(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
+  using C = Config<XT, NT, RT>;
   int per_sm = 0;
-  cudaError_t e = ctas_per_sm_once<gemv_int4_kernel<XT, GPB, NT>>(kThreads, C::kSmem, &per_sm);
+  cudaError_t e = ctas_per_sm_once<gemv_int4_kernel<XT, GPB, NT, RT, ZERO>>(kThreads, C::kSmem, &per_sm);
   if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (api_map_codes(&map, p.w.q, (p.K + 1) / 2, p.N, p.w.ldq, kInt4BoxBytes, 16 * RT, CU_TENSOR_MAP_SWIZZLE_64B) != BS_OK)
+    return cudaErrorInvalidValue;
   const bool xvec = (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 && (p.ldx * sizeof(XT)) % 16 == 0;
-  const long long tiles = (p.N + kInt4TileRows - 1) / kInt4TileRows;
-  const int S = splits_for(tiles, (p.K + 127) / 128, static_cast<long long>(per_sm) * sms);
-  cudaLaunchAttribute attr[2];
+  const long long blocks = (p.K + 127) / 128;
+  int kw = 1;  // warps that split K: all eight where there are as many blocks
+  while (kw < kWarps && 2 * kw <= blocks) kw *= 2;
+  const long long rows = 16 * RT * (kWarps / kw), tiles = (p.N + rows - 1) / rows;
+  const long long slots = static_cast<long long>(per_sm) * sms;
+  cudaLaunchAttribute attr[1];
   // programmatic dependent launch: the prologue may overlap the previous kernel
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < slots ? tiles : slots), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemv_int4_kernel<XT, GPB, NT>, q, p, S, xvec, err);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemv_int4_kernel<XT, GPB, NT, RT, ZERO>, map, p, kw, static_cast<uint32_t>(tiles), xvec, err);
+}
+
+template <typename XT, int GPB, int NT, int RT>
+cudaError_t launch_one(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
+  return p.w.zero ? launch_zero<XT, GPB, NT, RT, true>(p, sms, err, stream) : launch_zero<XT, GPB, NT, RT, false>(p, sms, err, stream);
+}
+
+// Rows per warp: 64 (32 with four tiles of activation rows, whose fragments take
+// the registers) share a block's activations, 16 give more CTAs.  Measured,
+// 64 against 16: 7168 x 2048, 8 rows 6.9 against 8.2 us; 131072 x 5120, one row
+// 86 against 135; 2900 x 1500 7.6 against 6.2; 1024 x 4096 8.0 against 5.5.
+// fp32 activations, split in registers, pay for 64 rows earlier: 8191 x 8208,
+// 5 rows 30 against 64.
+template <typename XT, int GPB, int NT>
+cudaError_t launch_rows(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
+  constexpr int RT = NT == 4 ? 2 : 4;
+  const long long enough = (sizeof(XT) == 2 ? 32LL : 16LL) * sms;
+  return p.N >= enough ? launch_one<XT, GPB, NT, RT>(p, sms, err, stream) : launch_one<XT, GPB, NT, 1>(p, sms, err, stream);
 }
 
 template <typename XT, int GPB>
-cudaError_t launch_tiles(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
-  if (p.M <= 8) return launch_one<XT, GPB, 1>(p, q, sms, err, stream);
-  return p.M <= 16 ? launch_one<XT, GPB, 2>(p, q, sms, err, stream) : launch_one<XT, GPB, 4>(p, q, sms, err, stream);
+cudaError_t launch_tiles(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
+  if (p.M <= 8) return launch_rows<XT, GPB, 1>(p, sms, err, stream);
+  if constexpr (sizeof(XT) == 2) {
+    if (p.M > 16) return launch_rows<XT, GPB, 4>(p, sms, err, stream);
+  }
+  return launch_rows<XT, GPB, 2>(p, sms, err, stream);
 }
 
 template <typename XT>
-cudaError_t launch_group(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
-  if (p.w.group == 128) return launch_tiles<XT, 1>(p, q, sms, err, stream);
-  return p.w.group == 64 ? launch_tiles<XT, 2>(p, q, sms, err, stream) : launch_tiles<XT, 4>(p, q, sms, err, stream);
+cudaError_t launch_group(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
+  if (p.w.group == 128) return launch_tiles<XT, 1>(p, sms, err, stream);
+  return p.w.group == 64 ? launch_tiles<XT, 2>(p, sms, err, stream) : launch_tiles<XT, 4>(p, sms, err, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_gemv_int4(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream) {
-  return p.x_bf16 ? launch_group<__nv_bfloat16>(p, q, sms, err, stream) : launch_group<float>(p, q, sms, err, stream);
+cudaError_t launch_gemv_int4(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
+  if (p.x_bf16) return launch_group<__nv_bfloat16>(p, sms, err, stream);
+  // fp32: 16 activation rows per launch (three parts of more would not fit the registers)
+  for (int m = 0; m < p.M; m += 16) {
+    Int4Product h = p;
+    h.x = static_cast<const float*>(p.x) + m * p.ldx;
+    h.out = static_cast<char*>(p.out) + m * p.ldo * (p.out_bf16 ? 2 : 4);
+    h.M = p.M - m < 16 ? p.M - m : 16;
+    const cudaError_t e = launch_group<float>(h, sms, err, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace bsg

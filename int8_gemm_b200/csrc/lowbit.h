@@ -56,9 +56,8 @@ struct Int4Product {
   int M;
   long long N, K;
 };
-constexpr int kInt4TileRows = 256;  // matrix rows of a CTA's tile, and
-constexpr int kInt4TileBytes = 64;  // bytes of a row per stage: the box of the tensor map of q (64-byte swizzle)
-cudaError_t launch_gemv_int4(const Int4Product& p, const CUtensorMap& q, int sms, uint32_t* err, cudaStream_t stream);
+constexpr int kInt4BoxBytes = 64;  // bytes of a matrix row per tensor copy (64-byte swizzle)
+cudaError_t launch_gemv_int4(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream);
 
 // ---- lookup -----------------------------------------------------------------
 // out[t, :] = alpha * table[tokens[t], :]; tokens null: row t itself.
