@@ -334,22 +334,18 @@ __global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
         for (int e = 0; e < 4; ++e)
           mine[(8 * j + 2 * t + e % 2) * C::kPitch + 16 * i + 8 * (e / 2) + gr] = acc[i][j][e];
     __syncthreads();
-    // kThreads is a multiple of the tile's rows, so a thread keeps its row
-    const int r = threadIdx.x & (tile_rows - 1);
-    const long long n = static_cast<long long>(tile) * tile_rows + r;
-    if (n < p.N) {
-      const float bias = p.bias ? p.bias[n] : 0.f;
-      const int m_step = kThreads / tile_rows;
-      int m = threadIdx.x / tile_rows;
+    const int rows_log2 = __ffs(tile_rows) - 1;  // a power of two
+    for (int i = threadIdx.x; i < p.M << rows_log2; i += kThreads) {
+      const int m = i >> rows_log2, r = i & (tile_rows - 1);
+      const long long n = static_cast<long long>(tile) * tile_rows + r;
+      if (n >= p.N) continue;
       const float* from = sums + ((r / (16 * RT)) * kw * 8 * NT + m) * C::kPitch + (r & (16 * RT - 1));
-      for (; m < p.M; m += m_step, from += m_step * C::kPitch) {
-        float y = from[0];
-        for (int w = 1; w < kw; ++w) y += from[w * 8 * NT * C::kPitch];
-        y += bias;
-        const long long o = m * p.ldo + n;
-        if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
-        else static_cast<float*>(p.out)[o] = y;
-      }
+      float y = from[0];
+      for (int w = 1; w < kw; ++w) y += from[w * 8 * NT * C::kPitch];
+      if (p.bias) y += p.bias[n];
+      const long long o = m * p.ldo + n;
+      if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+      else static_cast<float*>(p.out)[o] = y;
     }
     __syncthreads();
   }
