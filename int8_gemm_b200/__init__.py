@@ -26,6 +26,7 @@ The quantisers are also available as ``quantize_fp8_1x128``, ``quantize_fp8_t``,
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -621,17 +622,20 @@ def _int4_args(q, scale, zero, K: int, group: int):
     return N, (q.data_ptr(), ldq, scale.data_ptr(), _in_code(scale, "scale"), lds, zp, ldz, group)
 
 
-def _rows_out(out, shape: tuple, dtype: torch.dtype, index: int, device) -> torch.Tensor:
-    """`out`, or a new tensor of `shape` whose rows start on 16-byte boundaries."""
+def _rows_out(out, shape: tuple, dtype: torch.dtype, index: int, device):
+    """(tensor, row stride): `out` read as rows of equal distance, or a new tensor of `shape` whose rows start on
+    16-byte boundaries."""
     if out is None:
-        if shape[-1] * dtype.itemsize % 16 == 0:
-            return torch.empty(*shape, dtype=dtype, device=device)  # sizes one by one: 0.7 us less than as a tuple
-        return _empty_out(shape[:-1], shape[-1], dtype, device)
+        D = shape[-1]
+        if D * dtype.itemsize % 16 == 0:
+            return torch.empty(*shape, dtype=dtype, device=device), D  # sizes one by one: 0.7 us less than as a tuple
+        out = _empty_out(shape[:-1], D, dtype, device)
+        return out, out.stride(-2) if len(shape) > 1 else D
     if _same_device(out) != index:
         raise BsgemmError(BS_ERR_DEVICE, f"out is on {out.device}, the inputs on cuda:{index}")
     if out.dtype != dtype or out.shape != shape:
         raise BsgemmError(BS_ERR_SHAPE, f"out must be {list(shape)} of {dtype}, got {list(out.shape)} of {out.dtype}")
-    return out
+    return out, _flat_rows(out, math.prod(shape[:-1]), shape[-1], "out")
 
 
 def _flat_rows(t: torch.Tensor, T: int, D: int, name: str) -> int:
@@ -667,7 +671,7 @@ def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype
     N, K = x.shape
     G = -(-K // group)
     if q is None:
-        q = _rows_out(None, (N, (K + 1) // 2), torch.uint8, index, device)
+        q, _ = _rows_out(None, (N, (K + 1) // 2), torch.uint8, index, device)
     if scale is None:
         scale = torch.empty(N, G, dtype=scale_dtype, device=device)
     elif scale.dtype != scale_dtype:
@@ -690,8 +694,8 @@ def bs_dequantize_int4(q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor 
     K = 2 * q.shape[-1] if K is None else int(K)
     N, w = _int4_args(q, scale, zero, K, group)
     code = _float_out(out_dtype)
-    out = _rows_out(out, (N, K), out_dtype, index, q.device)
-    _launch(index, lib().bs_dequantize_int4, *w, out.data_ptr(), code, _unit_rows(out, "out"), N, K)
+    out, ldo = _rows_out(out, (N, K), out_dtype, index, q.device)
+    _launch(index, lib().bs_dequantize_int4, *w, out.data_ptr(), code, ldo, N, K)
     return out
 
 
@@ -716,8 +720,7 @@ def bs_gemv_int4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, zero: to
             raise BsgemmError(BS_ERR_SHAPE, f"bias must be a contiguous float32 [{N}]")
         bp = bias.data_ptr()
     code = _float_out(out_dtype)
-    out = _rows_out(out, (M, N) if x2 is x else (N,), out_dtype, index, x.device)
-    ldo = _unit_rows(out if x2 is x else out.unsqueeze(0), "out")
+    out, ldo = _rows_out(out, (M, N) if x2 is x else (N,), out_dtype, index, x.device)
     _launch(index, lib().bs_gemv_int4, x.data_ptr(), xd, ldx, *w, bp, out.data_ptr(), code, ldo, M, N, K)
     return out
 
@@ -782,8 +785,7 @@ def bs_embedding(tokens: torch.Tensor, table: torch.Tensor, scale: torch.Tensor 
         else:
             raise BsgemmError(BS_ERR_DTYPE, f"unknown table format {format!r}")
     T = tok.numel()
-    out = _rows_out(out, (*tokens.shape, D), out_dtype, index, tokens.device)
-    ldo = _flat_rows(out, T, D, "out")
+    out, ldo = _rows_out(out, (*tokens.shape, D), out_dtype, index, tokens.device)
     _launch(index, lib().bs_embedding, tok.data_ptr(), td, T, table.data_ptr(), fmt, ld, sp, sd, lds, zp, ldz, group, V, D,
             float(alpha), out.data_ptr(), code, ldo)
     return out
@@ -811,12 +813,12 @@ def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, a
         raise BsgemmError(BS_ERR_NULL, "accumulate adds to out, which must be given")
     T, D = tok.numel(), grad.shape[-1]
     ldg = _flat_rows(grad, T, D, "grad")
-    out = _rows_out(out, (V, D), out_dtype, index, device)
+    out, ldo = _rows_out(out, (V, D), out_dtype, index, device)
     h = lib()
     n = h.bs_embedding_grad_workspace(T, V, D)
     ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None  # the allocator's blocks are 512-byte aligned
     _launch(index, h.bs_embedding_grad, tok.data_ptr(), td, T, grad.data_ptr(), gd, ldg, V, D, float(alpha),
-            -1 if padding_idx is None else int(padding_idx), out.data_ptr(), code, _unit_rows(out, "out"),
+            -1 if padding_idx is None else int(padding_idx), out.data_ptr(), code, ldo,
             1 if accumulate else 0, None if ws is None else ws.data_ptr(), n)
     return out
 

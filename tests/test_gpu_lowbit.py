@@ -93,6 +93,21 @@ def test_quantize_bit_exact(N, K, group, dtype, scale_dtype, asym):
         assert same(w, torch.from_numpy(ref.values(codes, scale, zero, group)).to(out_dtype))
 
 
+@pytest.mark.parametrize("dtype,scale_dtype,asym,group", [(BF, F, False, 128), (F, BF, True, 32), (BF, BF, True, 64)])
+def test_quantize_large_bit_exact(dtype, scale_dtype, asym, group):
+    """More than 2^24 elements: the kernel with two passes per warp."""
+    N, K = 4100, 4099
+    x = _weights(N, K, 17, dtype)
+    q, s, z = bs.bs_quantize_int4(x.to(DEV), group=group, scale_dtype=scale_dtype, asymmetric=asym)
+    codes, scale, zero = ref.quantize_int4(x, group, scale_dtype == BF, asym)
+    assert np.array_equal(s.float().cpu().numpy(), scale)
+    assert np.array_equal(q.cpu().numpy(), ref.pack(codes, zero, group))
+    if asym:
+        assert np.array_equal(z.cpu().numpy(), zero)
+    w = bs.bs_dequantize_int4(q, s, z, K=K, group=group, out_dtype=dtype)
+    assert same(w, torch.from_numpy(ref.values(codes, scale, zero, group)).to(dtype))
+
+
 @pytest.mark.parametrize("asym", [False, True])
 def test_quantize_ranges_from_subnormal_to_huge(asym):
     """Scales that underflow to one, subnormal scales, scales on both sides of the fast quotient's range, the largest
@@ -350,6 +365,17 @@ def test_lookup_bit_exact(D, out_dtype, fmt):
             got = bs.bs_embedding(tokens.to(DEV), table, alpha=alpha, out_dtype=out_dtype, **kw)
             assert got.shape == (len(TOKENS), D)
             assert same(got, torch.from_numpy(ref.lookup(tokens.numpy(), values, alpha)).to(out_dtype))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f32", "e4m3", "e8m0", "int4"])
+@pytest.mark.parametrize("out_dtype", [BF, F])
+@pytest.mark.parametrize("T,D", [(1100, 5120), (2500, 1001), (40000, 72), (600000, 4)])
+def test_lookup_large_bit_exact(T, D, out_dtype, fmt):
+    """Outputs of more than 4 MB: several pieces per lane, whole runs and ragged ones."""
+    values, table, kw = _table(fmt, 400, D, D)
+    tokens = torch.randint(-5, 405, (T,), generator=_gen(T))
+    got = bs.bs_embedding(tokens.to(DEV), table, alpha=1.7, out_dtype=out_dtype, **kw)
+    assert same(got, torch.from_numpy(ref.lookup(tokens.numpy(), values, 1.7)).to(out_dtype))
 
 
 @pytest.mark.parametrize("T", [0, 1, 2, 255, 4097])

@@ -206,3 +206,17 @@ def test_reference_gradient_is_the_lookup_s():
             # the loss sum(c * lookup) is linear in the table, so a difference is its derivative
             assert np.sum(c * ref.lookup(tokens, up, 2.0)) - np.sum(c * ref.lookup(tokens, table, 2.0)) == d[r, j]
     assert n.tolist() == [3, 0, 0, 2, 0, 1] and np.all(S >= np.abs(d))
+
+
+@pytest.mark.parametrize("div,r", [(7, float.fromhex("0x1.24924ap-3")), (15, float.fromhex("0x1.111112p-4"))])
+def test_quotients_by_the_range_constants(div, r):
+    """The quantiser's a / 7 and a / 15 (a constant reciprocal and Markstein's correction step) for every significand;
+    the steps scale with the exponent where nothing under- or overflows.  The fma is taken in extended precision."""
+    assert np.float32(r) == np.float32(1) / np.float32(div) and np.finfo(np.longdouble).nmant >= 63
+    for lo in range(0, 1 << 23, 1 << 20):
+        a = (np.arange(lo, lo + (1 << 20), dtype=np.int64) + (1 << 23)).astype(np.float32) * np.float32(2.0**-23)
+        q1 = (a * np.float32(r)).astype(np.float32)
+        rem = a.astype(np.float64) - q1.astype(np.float64) * div  # exact, and an fp32 number
+        assert np.array_equal(rem, rem.astype(np.float32))
+        q = (q1.astype(np.longdouble) + rem.astype(np.longdouble) * np.longdouble(r)).astype(np.float32)
+        assert np.array_equal(q, a / np.float32(div))
