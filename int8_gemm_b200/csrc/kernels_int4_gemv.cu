@@ -159,7 +159,12 @@ __global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kWarps][C::kStages];
   __shared__ int abort_flag;
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  if (pad + C::kSmem - 1024 > dynamic_smem_bytes()) {  // never touch memory the launch did not provide
+    if (threadIdx.x == 0) record_error(err, kErrSmemTooSmall);
+    return;
+  }
+  uint8_t* base = smem_raw + pad;
   float* sums = reinterpret_cast<float*>(base + C::kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
   uint8_t* ring = base + warp * C::kStages * C::kBoxBytes;
