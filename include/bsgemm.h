@@ -410,7 +410,8 @@ bs_status bs_dequantize_int4(const void* q, int64_t ldq, const void* scale, bs_i
  *
  * The sum of a group is formed before its scale is applied; sums are fp32, in
  * an order that depends on the sizes alone, and rounded once to the output
- * type.  Codes are never rounded and fp32 activations keep all their bits.
+ * type.  Codes are never rounded, and fp32 activations of at least 2^-100 in
+ * magnitude keep all their bits.
  *   x      bf16 or fp32 [M, K], 1 <= M <= 32, row m at x + m*ldx (ldx >= K),
  *          aligned to its element size
  *   q      codes [N, K] as above, 16-byte aligned with ldq a multiple of 16

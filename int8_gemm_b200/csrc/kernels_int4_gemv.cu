@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
         }
       }
       if (ok) ok = wait_bounded(&full[warp][st], phase, &abort_flag, err, kErrTimeout | kRoleConsumer | kWaitStageFull);
+      ok = __all_sync(0xffffffffu, ok);  // the lanes of a warp go on, or give up, together
       if (!ok) break;
       const uint8_t* box = ring + st * C::kBoxBytes;
 #pragma unroll

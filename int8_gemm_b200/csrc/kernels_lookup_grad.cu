@@ -362,14 +362,28 @@ __device__ __forceinline__ void write_row(const RowArgs& a, uint32_t v, long lon
   const long long left = a.D - d;
   float y[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) y[i] = a.alpha * sum[i];
-  if (!a.accumulate && a.ovec && left >= E) {
+  for (int i = 0; i < E; ++i) y[i] = __fmul_rn(a.alpha, sum[i]);
+  if (a.ovec && left >= E) {
     if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
-      for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+      for (int i = 0; i < E; i += 4) {
+        float4 v = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        if (a.accumulate) {
+          const float4 old = *reinterpret_cast<const float4*>(p + i);
+          v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+        }
+        *reinterpret_cast<float4*>(p + i) = v;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < E; i += 4) {
+        if (a.accumulate) {
+          const uint2 old = *reinterpret_cast<const uint2*>(p + i);
+          y[i] += __uint_as_float(old.x << 16);
+          y[i + 1] += __uint_as_float(old.x & 0xFFFF0000u);
+          y[i + 2] += __uint_as_float(old.y << 16);
+          y[i + 3] += __uint_as_float(old.y & 0xFFFF0000u);
+        }
         const __nv_bfloat162 h0 = __floats2bfloat162_rn(y[i], y[i + 1]), h1 = __floats2bfloat162_rn(y[i + 2], y[i + 3]);
         *reinterpret_cast<uint2*>(p + i) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
