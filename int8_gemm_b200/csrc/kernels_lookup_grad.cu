@@ -50,7 +50,7 @@ constexpr int kThreads = 256;
 constexpr int kZeroRows = 32;  // rows per zeroing CTA of rows_kernel
 constexpr int kSmallT = 512;         // tokens that the single launch takes (D = 512: 200 tokens 16 us, 1000 tokens 31 us against 21)
 constexpr int kRankTokens = 32, kRankWays = kThreads / kRankTokens;  // per CTA of rank_kernel; threads per token
-constexpr long long kRankMaxT = 4096;  // tokens up to which it is the faster sort (whole gradient, D = 512: 27 us against 30; 8192: 36 against 35)
+constexpr long long kRankMaxT = 4096;  // tokens up to which it is the faster sort (whole gradient, D = 512: 26 us against 31; 6000 tokens: 32 against 31)
 constexpr int kMarkRows = 16 * 8192;  // rows marked at a time: a 16 KB bitmap
 
 // Workspace: two (key, position) buffers of T pairs, then the partial sums of
@@ -122,25 +122,27 @@ struct SortArgs {
   int passes, bits;  // pass i takes `bits` bits; reads buffer i & 1 (pass 0: the tokens) and writes the other
 };
 
-// The pairs [lo, hi) of one warp, four rounds of 32 loaded at a time.
-template <typename Fn>
-__device__ __forceinline__ void each_pair(const SortArgs& a, int pass, uint32_t lo, uint32_t hi, Fn fn) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t* kin = a.key[pass & 1];
-  for (uint32_t i0 = lo; i0 < hi; i0 += 128) {
-    uint32_t k[4];
+// Four rounds of 32 pairs of one warp, from i0 on.
+struct Batch {
+  uint32_t k[4], p[4];
+
+  __device__ __forceinline__ void load(const SortArgs& a, int pass, uint32_t i0, uint32_t hi) {
+    const uint32_t* kin = a.key[pass & 1];
+    const uint32_t* pin = a.pos[pass & 1];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t i = i0 + 32 * r + lane;
+      const uint32_t i = i0 + 32 * r + (threadIdx.x & 31);
       k[r] = i >= hi ? 0u : (pass == 0 ? a.in.key(i) : kin[i]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint32_t i = i0 + 32 * r + lane;
-      if (i0 + 32 * r < hi) fn(i, i < hi, k[r]);
+      p[r] = i >= hi || pass == 0 ? i : pin[i];
     }
   }
-}
+  template <typename Fn>
+  __device__ __forceinline__ void each(uint32_t i0, uint32_t hi, Fn fn) const {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (i0 + 32 * r < hi) fn(i0 + 32 * r + (threadIdx.x & 31) < hi, k[r], p[r]);
+  }
+};
 
 __device__ __forceinline__ void sort_pairs(const SortArgs& a, uint32_t (*hist)[kMaxDigits]) {
   __shared__ uint32_t total[kMaxDigits];  // this CTA's digit counts, read by the whole cluster
@@ -151,7 +153,7 @@ __device__ __forceinline__ void sort_pairs(const SortArgs& a, uint32_t (*hist)[k
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // this warp's pairs [lo, hi): runs of a multiple of 32, in (CTA, warp) order
   const uint32_t runs = kSortCtas * kSortWarps, T = a.in.T;
-  const uint32_t per = (T / runs + 32) / 32 * 32;
+  const uint32_t per = ((T + runs - 1) / runs + 31) / 32 * 32;
   const uint64_t lo64 = static_cast<uint64_t>(rank * kSortWarps + warp) * per;
   const uint32_t lo = lo64 < T ? static_cast<uint32_t>(lo64) : T;
   const uint32_t hi = lo64 + per < T ? static_cast<uint32_t>(lo64 + per) : T;
@@ -161,17 +163,22 @@ __device__ __forceinline__ void sort_pairs(const SortArgs& a, uint32_t (*hist)[k
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = a.bits * pass;
-    const uint32_t* pin = a.pos[pass & 1];
     uint32_t* kout = a.key[(pass & 1) ^ 1];
     uint32_t* pout = a.pos[(pass & 1) ^ 1];
     for (int d = lane; d < digits; d += 32) hist[warp][d] = 0;
     __syncwarp();
-    each_pair(a, pass, lo, hi, [&](uint32_t, bool in, uint32_t k) {
-      const uint32_t d = in ? (k >> shift) & mask : kMaxDigits;  // lanes past the end match one another only
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      if (in && (same & below) == 0) hist[warp][d] += __popc(same);
-      __syncwarp();
-    });
+    Batch first;  // kept for the second sweep: all there is up to 32768 pairs
+    first.load(a, pass, lo, hi);
+    for (uint32_t i0 = lo; i0 < hi; i0 += 128) {
+      Batch batch = first;
+      if (i0 != lo) batch.load(a, pass, i0, hi);
+      batch.each(i0, hi, [&](bool in, uint32_t k, uint32_t) {
+        const uint32_t d = in ? (k >> shift) & mask : kMaxDigits;  // lanes past the end match one another only
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (in && (same & below) == 0) hist[warp][d] += __popc(same);
+        __syncwarp();
+      });
+    }
     __syncthreads();
     if (tid < digits) {  // counts of the warps before each warp, and the CTA's total
       uint32_t sum = 0;
@@ -209,19 +216,23 @@ __device__ __forceinline__ void sort_pairs(const SortArgs& a, uint32_t (*hist)[k
       base[tid] += pre;
     }
     __syncthreads();
-    each_pair(a, pass, lo, hi, [&](uint32_t i, bool in, uint32_t k) {
-      const uint32_t d = in ? (k >> shift) & mask : kMaxDigits;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      uint32_t at = 0;
-      if (in) at = base[d] + hist[warp][d] + __popc(same & below);
-      __syncwarp();
-      if (in) {
-        if ((same & below) == 0) hist[warp][d] += __popc(same);
-        kout[at] = k;
-        pout[at] = pass == 0 ? i : pin[i];
-      }
-      __syncwarp();
-    });
+    for (uint32_t i0 = lo; i0 < hi; i0 += 128) {
+      Batch batch = first;
+      if (i0 != lo) batch.load(a, pass, i0, hi);
+      batch.each(i0, hi, [&](bool in, uint32_t k, uint32_t p) {
+        const uint32_t d = in ? (k >> shift) & mask : kMaxDigits;
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        uint32_t at = 0;
+        if (in) at = base[d] + hist[warp][d] + __popc(same & below);
+        __syncwarp();
+        if (in) {
+          if ((same & below) == 0) hist[warp][d] += __popc(same);
+          kout[at] = k;
+          pout[at] = p;
+        }
+        __syncwarp();
+      });
+    }
     // the pairs written here are read by other CTAs in the next pass, and this
     // CTA's totals are no longer read by any
     cluster.sync();
