@@ -670,17 +670,22 @@ def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype
         raise BsgemmError(BS_ERR_SHAPE, f"group must be 32, 64 or 128, got {group}")
     N, K = x.shape
     G = -(-K // group)
+    given = q is not None or scale is not None or zero is not None
+    ldq = 0
     if q is None:
-        q, _ = _rows_out(None, (N, (K + 1) // 2), torch.uint8, index, device)
+        q, ldq = _rows_out(None, (N, (K + 1) // 2), torch.uint8, index, device)
     if scale is None:
         scale = torch.empty(N, G, dtype=scale_dtype, device=device)
     elif scale.dtype != scale_dtype:
         raise BsgemmError(BS_ERR_DTYPE, f"scale must be {scale_dtype}, got {scale.dtype}")
     if asymmetric and zero is None:
         zero = torch.empty(N, G, dtype=torch.uint8, device=device)
-    rows, w = _int4_args(q, scale, zero, K, group)
-    if rows != N:
-        raise BsgemmError(BS_ERR_SHAPE, f"q must have {N} rows, got {rows}")
+    if given:
+        rows, w = _int4_args(q, scale, zero, K, group)
+        if rows != N:
+            raise BsgemmError(BS_ERR_SHAPE, f"q must have {N} rows, got {rows}")
+    else:
+        w = (q.data_ptr(), ldq, scale.data_ptr(), _IN_CODE[scale_dtype], G, zero.data_ptr() if asymmetric else None, G, group)
     _launch(index, lib().bs_quantize_int4, x.data_ptr(), xd, N, K, ldx, *w)
     return q, scale, zero
 

@@ -14,8 +14,8 @@
 // A lane holds 16 consecutive elements, so group / 16 lanes share a group and
 // reduce its range with shuffles; a warp covers 512 elements of a row per
 // pass and has one or two passes' loads in flight.  5120 x 8192 bf16 in groups
-// of 128 takes 24.6 us, 4.3 TB/s; 5120 x 8192 fp32 in groups of 32 with zero points
-// 32 us, 6.1 TB/s.  Elements past K read as zero,
+// of 128 takes 21.9 us, 4.8 TB/s; 5120 x 8192 fp32 in groups of 32 with zero points
+// 31.4 us, 6.2 TB/s.  Elements past K read as zero,
 // which changes no range and whose code is the zero point, so the unused
 // nibble of an odd row's last byte stands for the value zero.
 #include <cuda_bf16.h>
@@ -30,19 +30,48 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarpElems = 512;
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Elements k .. k+15 of a row (zero at or past K); `vec`: all inside the row
-// and 16-byte aligned.
+// Elements k .. k+15 of a row, as stored.
 template <typename InT>
-__device__ __forceinline__ void load16(const InT* row, long long k, long long K, bool vec, float (&v)[16]) {
-  if (vec) {
-    constexpr int kPer = 16 / sizeof(InT);
+struct Sixteen {
+  uint4 r[sizeof(InT)];
+
+  // Those at or past K are zero; `vec`: all inside the row and 16-byte aligned.
+  __device__ __forceinline__ void load(const InT* row, long long k, long long K, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < 16 / kPer; ++i) {
-      const uint4 t = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
-      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+      for (int i = 0; i < static_cast<int>(sizeof(InT)); ++i) r[i] = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
+      return;
+    }
+    uint32_t w[4 * sizeof(InT)] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (k + i >= K) continue;
+      if constexpr (sizeof(InT) == 4) w[i] = __float_as_uint(row[k + i]);
+      else w[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(row[k + i])) << (16 * (i % 2));
+    }
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(InT)); ++i) r[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+
+  // Their largest magnitude (of bf16 pairs two at a time).
+  __device__ __forceinline__ float amax() const {
+    if constexpr (sizeof(InT) == 4) {
+      float v[16], m = 0.f;
+      values(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+      return m;
+    } else {
+      uint32_t m = max_abs_bf16x2(max_abs_bf16x2(r[0].x, r[0].y), max_abs_bf16x2(r[0].z, r[0].w));
+      m = max_abs_bf16x2(m, max_abs_bf16x2(max_abs_bf16x2(r[1].x, r[1].y), max_abs_bf16x2(r[1].z, r[1].w)));
+      return fmaxf(__uint_as_float((m << 16) & 0x7FFFFFFFu), __uint_as_float(m & 0x7FFF0000u));
+    }
+  }
+
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(InT)); ++i) {
+      const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (sizeof(InT) == 4) {
@@ -53,11 +82,8 @@ __device__ __forceinline__ void load16(const InT* row, long long k, long long K,
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = k + i < K ? to_f32(row[k + i]) : 0.f;
   }
-}
+};
 
 // a / 7 and a / 15, correctly rounded, by Markstein's correction step (see
 // quotient_rn in group_quant.cuh) where nothing under- or overflows: the
@@ -124,7 +150,7 @@ __device__ __forceinline__ void codes16(const float (&v)[16], float s, float z, 
 }
 
 template <typename InT, typename ScaleT, bool ASYM, int LANES, int kPasses>
-__global__ void __launch_bounds__(kThreads, kPasses == 1 ? 6 : 4)
+__global__ void __launch_bounds__(kThreads, kPasses == 1 || sizeof(InT) == 2 ? 6 : 5)
     quantize_int4_kernel(const InT* __restrict__ x, long long N, long long K, long long ldx, uint8_t* __restrict__ q,
                          long long ldq, ScaleT* __restrict__ scale, long long lds, uint8_t* __restrict__ zero,
                          long long ldz) {
@@ -139,24 +165,26 @@ __global__ void __launch_bounds__(kThreads, kPasses == 1 ? 6 : 4)
   uint8_t* qrow = q + n * ldq;
   const bool row_vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
   const bool q_vec = (reinterpret_cast<uintptr_t>(qrow) & 7u) == 0;
-  float v[kPasses][16];
+  Sixteen<InT> raw[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const long long k = k0 + p * kWarpElems;
-    load16<InT>(row, k, K, row_vec && k + 16 <= K, v[p]);
+    raw[p].load(row, k, K, row_vec && k + 16 <= K);
   }
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const long long k = k0 + p * kWarpElems;
+    float v[16];
+    raw[p].values(v);
     float lo = 0.f, hi = 0.f;
+    if constexpr (ASYM) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if constexpr (ASYM) {
-        lo = fminf(lo, v[p][i]);
-        hi = fmaxf(hi, v[p][i]);
-      } else {
-        hi = fmaxf(hi, fabsf(v[p][i]));
+      for (int i = 0; i < 16; ++i) {
+        lo = fminf(lo, v[i]);
+        hi = fmaxf(hi, v[i]);
       }
+    } else {
+      hi = raw[p].amax();
     }
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) {
@@ -170,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, kPasses == 1 ? 6 : 4)
     if constexpr (ASYM) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
     uint32_t w[2];
     if (__all_sync(0xffffffffu, quotient_fast_range(s) && hi <= 3.40282347e38f)) {
-      codes16<ASYM, true>(v[p], s, z, w);
+      codes16<ASYM, true>(v, s, z, w);
     } else {
-      codes16<ASYM, false>(v[p], s, z, w);
+      codes16<ASYM, false>(v, s, z, w);
     }
     if (k < K) {
       if (lane % LANES == 0) {
@@ -207,8 +235,8 @@ cudaError_t launch_passes(const void* x, long long N, long long K, long long ldx
 }
 
 // Two passes per warp for large matrices, one for up to 2^24 elements: more warps
-// (1024 x 4096 fp32 4.9 against 6.2 us, 2085 x 4099 bf16 6.9 against 9.1; 5120 x
-// 8192 bf16 25.3 against 24.6).
+// (1024 x 4096 fp32 5.5 against 6.2 us, 2085 x 4099 bf16 7.5 against 9.1; 5120 x
+// 8192 bf16 25.3 against 21.9).
 template <typename InT, typename ScaleT, bool ASYM, int LANES>
 cudaError_t launch_one(const void* x, long long N, long long K, long long ldx, uint8_t* q, long long ldq, void* scale,
                        long long lds, uint8_t* zero, long long ldz, cudaStream_t stream) {
