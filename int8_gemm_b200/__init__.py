@@ -26,6 +26,7 @@ The quantisers are also available as ``quantize_fp8_1x128``, ``quantize_fp8_t``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -796,6 +797,11 @@ def bs_embedding(tokens: torch.Tensor, table: torch.Tensor, scale: torch.Tensor 
     return out
 
 
+@functools.lru_cache(maxsize=64)
+def _grad_workspace(T: int, V: int, D: int) -> int:
+    return int(lib().bs_embedding_grad_workspace(T, V, D))
+
+
 def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, alpha: float = 1.0,
                       padding_idx: int | None = None, out_dtype: torch.dtype = torch.float32,
                       out: torch.Tensor | None = None, accumulate: bool = False) -> torch.Tensor:
@@ -819,10 +825,9 @@ def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, a
     T, D = tok.numel(), grad.shape[-1]
     ldg = _flat_rows(grad, T, D, "grad")
     out, ldo = _rows_out(out, (V, D), out_dtype, index, device)
-    h = lib()
-    n = h.bs_embedding_grad_workspace(T, V, D)
+    n = _grad_workspace(T, V, D)
     ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None  # the allocator's blocks are 512-byte aligned
-    _launch(index, h.bs_embedding_grad, tok.data_ptr(), td, T, grad.data_ptr(), gd, ldg, V, D, float(alpha),
+    _launch(index, lib().bs_embedding_grad, tok.data_ptr(), td, T, grad.data_ptr(), gd, ldg, V, D, float(alpha),
             -1 if padding_idx is None else int(padding_idx), out.data_ptr(), code, ldo,
             1 if accumulate else 0, None if ws is None else ws.data_ptr(), n)
     return out
