@@ -438,8 +438,8 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
  *   table    [V, D], row v at table + v*ld_table elements:
  *            BS_TABLE_BF16, BS_TABLE_F32   values; scale, zero and group unused
  *            BS_TABLE_E4M3, BS_TABLE_E4M3_E8M0  the codes of
- *              bs_quantize_fp8_1x128, with its scales (fp32 or e8m0 bytes) at
- *              scale[v*ld_scale + d/128]
+ *              bs_quantize_fp8_1x128, with its scales (fp32 or e8m0 bytes, 255
+ *              being NaN) at scale[v*ld_scale + d/128]
  *            BS_TABLE_INT4  a 4-bit matrix [V, D] as above (ld_table in bytes)
  *   out      [T, D], row stride ldo (>= D), BS_OUT_BF16 or BS_OUT_F32
  *

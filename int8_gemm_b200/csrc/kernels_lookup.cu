@@ -16,6 +16,7 @@
 #include <cuda_fp8.h>
 
 #include "lowbit.h"
+#include "sm100.cuh"
 
 namespace bsg {
 
@@ -24,10 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 
 enum class Fmt { kBF16, kF32, kE4M3, kE4M3E8M0, kInt4 };
-
-__device__ __forceinline__ float e8m0_value(uint8_t b) {
-  return __uint_as_float(b == 0 ? 0x00400000u : static_cast<uint32_t>(b) << 23);  // 2^-127 is subnormal
-}
 
 __device__ __forceinline__ long long token_at(const LookupArgs& a, long long t) {
   if (!a.tokens) return t;
@@ -138,7 +135,7 @@ struct Piece {
         v[i + 1] = x.y;
       }
     } else {
-      const float f = F == Fmt::kE4M3 ? __uint_as_float(s) : e8m0_value(static_cast<uint8_t>(s));
+      const float f = F == Fmt::kE4M3 ? __uint_as_float(s) : e8m0_to_f32(s);
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         const __half2_raw h =

@@ -414,6 +414,20 @@ def test_lookup_empty_table_and_single_row():
     assert bs.bs_embedding(tokens, torch.empty(5, 0, device=DEV)).shape == (3, 0)
 
 
+def test_lookup_e8m0_scale_bytes_at_their_ends():
+    """Byte 0 is 2^-127, byte 254 2^127 and byte 255 NaN, whatever the codes it scales."""
+    V, D = 4, 256
+    codes = torch.randint(0, 127, (V, D), generator=_gen(12), dtype=torch.uint8)
+    codes[:, ::5] = 0
+    scale = torch.tensor([[0, 1], [254, 127], [255, 127], [127, 255]], dtype=torch.uint8)
+    factor = torch.tensor([[2.0**-127, 2.0**-126], [2.0**127, 1], [float("nan"), 1], [1, float("nan")]])
+    want = torch.from_numpy(oracle.e4m3_table()[codes.numpy()].astype(np.float32)) * factor.repeat_interleave(128, 1)
+    for out_dtype in (BF, F):
+        got = bs.bs_embedding(torch.arange(V, device=DEV), codes.to(DEV), scale.to(DEV), format="e4m3", out_dtype=out_dtype)
+        # (compared as numbers: the bits of a NaN are not specified)
+        assert np.array_equal(got.float().cpu().numpy(), want.to(out_dtype).float().numpy(), equal_nan=True)
+
+
 # ---------------------------------------------------------------------------
 # gradient
 # ---------------------------------------------------------------------------
