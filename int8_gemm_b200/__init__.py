@@ -602,6 +602,8 @@ def _unit_rows(t: torch.Tensor, name: str) -> int:
 
 def _int4_args(q, scale, zero, K: int, group: int):
     """(rows, arguments from q to group) of a 4-bit matrix of K columns."""
+    if q is None or scale is None:
+        raise BsgemmError(BS_ERR_NULL, "a 4-bit matrix needs its codes and its scales")
     if group not in (32, 64, 128):
         raise BsgemmError(BS_ERR_SHAPE, f"group must be 32, 64 or 128, got {group}")
     if q.dtype != torch.uint8:
@@ -757,6 +759,8 @@ def bs_embedding(tokens: torch.Tensor, table: torch.Tensor, scale: torch.Tensor 
     out     [*tokens.shape, D] of out_dtype (bfloat16 or float32), rows of equal distance
     """
     index = _same_device(tokens, table, scale, zero)
+    if table is None:
+        raise BsgemmError(BS_ERR_NULL, "table must be given")
     code = _float_out(out_dtype)
     tok, td = _tokens_arg(tokens)
     sp, sd, lds, zp, ldz = None, 0, 0, None, 0
@@ -813,6 +817,8 @@ def bs_embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, a
     Tokens equal to padding_idx or outside the table contribute nothing.  The result is deterministic.
     """
     index, device = _same_device(tokens, grad, out), tokens.device
+    if grad is None:
+        raise BsgemmError(BS_ERR_NULL, "grad must be given")
     tok, td = _tokens_arg(tokens)
     gd, code, V = _in_code(grad, "grad"), _float_out(out_dtype), int(num_rows)
     if grad.dim() != tokens.dim() + 1 or grad.shape[:-1] != tokens.shape:

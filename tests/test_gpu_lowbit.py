@@ -331,6 +331,30 @@ def test_binding_refusals():
         assert e.value.status == status, (i, str(e.value))
 
 
+def test_binding_refuses_missing_tensors():
+    """A None in the place of a tensor that the call needs raises the library's error, in every place."""
+    _, (q, scale, _) = _matrix(8, 128, 64, 1)
+    x, t = torch.randn(2, 128, device=DEV), torch.zeros(2, dtype=torch.int64, device=DEV)
+    null, device = bs.BS_ERR_NULL, bs.BS_ERR_DEVICE
+    bad = [
+        (device, lambda: bs.bs_quantize_int4(None)),
+        (device, lambda: bs.bs_dequantize_int4(None, scale, group=64)),
+        (null, lambda: bs.bs_dequantize_int4(q, None, group=64)),
+        (device, lambda: bs.bs_gemv_int4(None, q, scale, group=64)),
+        (null, lambda: bs.bs_gemv_int4(x, None, scale, group=64)),
+        (null, lambda: bs.bs_gemv_int4(x, q, None, group=64)),
+        (device, lambda: bs.bs_embedding(None, x)),
+        (null, lambda: bs.bs_embedding(t, None)),
+        (null, lambda: bs.bs_embedding(t, None, scale, format="int4", group=64)),
+        (device, lambda: bs.bs_embedding_grad(None, x, 5)),
+        (null, lambda: bs.bs_embedding_grad(t, None, 5)),
+    ]
+    for i, (status, call) in enumerate(bad):
+        with pytest.raises(bs.BsgemmError) as e:
+            call()
+        assert e.value.status == status, (i, str(e.value))
+
+
 # ---------------------------------------------------------------------------
 # lookup
 # ---------------------------------------------------------------------------
