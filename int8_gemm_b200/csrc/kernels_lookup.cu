@@ -10,8 +10,9 @@
 // A token outside [0, V) gives a row of zeros and reads nothing.
 //
 // A lane handles pieces of 16 output bytes, the lanes of a warp side by side in
-// a row (in several where rows are short), four pieces' loads in flight; a
-// warp stays in its rows, so addresses are worked out once per row.
+// a row (in several where rows are short), the loads of one to eight pieces in
+// flight (unroll_of); a warp stays in its rows, so addresses are worked out once
+// per row.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -254,11 +255,29 @@ cudaError_t launch_unroll(const LookupArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Pieces per lane of outputs above 4 MB.  More hide the loads' latency until the
+// words they hold no longer fit the 64 registers of four blocks per SM: an fp32
+// table's piece for bf16 outputs is 8 words, an e4m3 one's 2 and its scale.  16640
+// rows of 5120 (and 8192 of 1001), us: fp32 to bf16 2 pieces 80.1 (25.6), 4
+// pieces, which spilled, 86.3 (31.9); e4m3 to bf16 4 pieces 48.6 (27.9), 8, which
+// spilled, 49.8 (31.2); e4m3 to fp32, no spill, 8 pieces 72.2, 4 pieces 82.6.
+// 4-bit tables keep 8, although that spills 64 bytes: 5120 x 8192 read whole to
+// bf16 22.2 against 23.7 with 4, to fp32 36.9 against 41.1, 16640 rows of 5120 to
+// fp32 78.5 against 86.1, to bf16 51.8 against 50.1.
+template <Fmt F, typename OutT>
+constexpr int unroll_of() {
+  constexpr bool bf16_out = sizeof(OutT) == 2;
+  if (F == Fmt::kBF16) return 4;
+  if (F == Fmt::kF32) return bf16_out ? 2 : 4;
+  if (F == Fmt::kE4M3 || F == Fmt::kE4M3E8M0) return bf16_out ? 4 : 8;
+  return 8;
+}
+
 // Small lookups spread over as many warps as there are (one piece per lane).
 template <Fmt F, typename OutT>
 cudaError_t launch_fmt(const LookupArgs& a, cudaStream_t stream) {
   const double bytes = static_cast<double>(a.T) * static_cast<double>(a.D) * sizeof(OutT);
-  return bytes <= 4e6 ? launch_unroll<F, OutT, 1>(a, stream) : launch_unroll<F, OutT, F == Fmt::kBF16 || F == Fmt::kF32 ? 4 : 8>(a, stream);
+  return bytes <= 4e6 ? launch_unroll<F, OutT, 1>(a, stream) : launch_unroll<F, OutT, unroll_of<F, OutT>()>(a, stream);
 }
 
 template <Fmt F>

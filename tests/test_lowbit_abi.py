@@ -3,6 +3,9 @@ reference definitions themselves, and the workspace size.  No GPU needed."""
 from __future__ import annotations
 
 import ctypes
+import os
+import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -157,6 +160,17 @@ def test_embedding_grad_workspace_covers_pairs_and_partials():
         assert size(T, 1000, D) >= 16 * T + 2 * -(-T // 32) * 4 * D
         assert size(T, 1000, D) == size(T, 5, D)
     assert size(2**31 - 1, 2**31 - 1, 2**31 - 1) > 2**58
+
+
+def test_lookup_kernels_keep_their_pieces_in_registers(tmp_path):
+    """No lookup kernel spills, but for those of 4-bit tables, where fewer pieces per lane measured slower."""
+    src = os.path.join(bsbuild.CSRC, "kernels_lookup.cu")
+    cmd = [bsbuild.nvcc(), *bsbuild.NVCC_FLAGS, "-Xptxas", "-v", "-c", src, "-o", str(tmp_path / "lookup.o")]
+    log = subprocess.run(cmd, capture_output=True, text=True, check=True).stderr
+    found = re.findall(r"Function properties for \S*lookup_kernelILNS0_3FmtE(\d)E(\S+)\n.*?(\d+) bytes spill stores", log)
+    assert len(found) == 5 * 2 * 2, log  # formats, output types, small and large
+    for fmt, rest, spilled in found:
+        assert int(spilled) <= (64 if fmt == "4" else 0), (fmt, rest, spilled)
 
 
 def test_binding_rejects_cpu_tensors():
