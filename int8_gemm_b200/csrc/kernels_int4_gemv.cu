@@ -70,17 +70,44 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int j, uint32_t off) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
+template <int W>
+struct Width {
+  static constexpr int value = W;
+};
+
 // Eight consecutive activations of a row, as read.
 template <typename XT>
 struct Eight {
   uint32_t r[2 * sizeof(XT)];
 
-  // From a 16-byte boundary, or zeros.
-  __device__ __forceinline__ void load16(const XT* p, bool in) {
+  // All of them from a boundary of W bytes, or zeros.  W = 2 (bf16): whole words
+  // and, where the row starts between two, an element at either end.
+  template <int W>
+  __device__ __forceinline__ void load_whole(const XT* p, bool in) {
+    constexpr int kWords = static_cast<int>(2 * sizeof(XT));
+    if constexpr (W == 16) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(XT)) / 2; ++i) {
-      const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
-      r[4 * i] = u.x, r[4 * i + 1] = u.y, r[4 * i + 2] = u.z, r[4 * i + 3] = u.w;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(p) + i / 4) : make_uint4(0, 0, 0, 0);
+        r[i] = u.x, r[i + 1] = u.y, r[i + 2] = u.z, r[i + 3] = u.w;
+      }
+    } else if constexpr (W == 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) r[i] = in ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : 0u;
+    } else {
+      static_assert(W == 2 && sizeof(XT) == 2, "fp32 rows start on 4-byte boundaries");
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      const bool odd = (reinterpret_cast<uintptr_t>(p) & 2u) != 0;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(h + (odd ? 1 : 0));
+      const uint32_t head = in && odd ? static_cast<uint32_t>(__ldg(h)) << 16 : 0u;
+      const uint32_t w0 = in ? __ldg(w) : 0u, w1 = in ? __ldg(w + 1) : 0u, w2 = in ? __ldg(w + 2) : 0u;
+      uint32_t tail = in && odd ? __ldg(h + 7) : 0u;
+      if (in && !odd) tail = __ldg(w + 3);
+      const uint32_t shift = odd ? 16 : 0;
+      r[0] = __funnelshift_l(head, w0, shift);
+      r[1] = __funnelshift_l(w0, w1, shift);
+      r[2] = __funnelshift_l(w1, w2, shift);
+      r[3] = __funnelshift_l(w2, tail, shift);
     }
   }
 
@@ -150,7 +177,7 @@ struct Side {
 
 template <typename XT, int GPB, int NT, int RT, bool ZERO>
 __global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
-    gemv_int4_kernel(const __grid_constant__ CUtensorMap tmq, const Int4Product p, int kw, uint32_t tiles, bool xvec,
+    gemv_int4_kernel(const __grid_constant__ CUtensorMap tmq, const Int4Product p, int kw, uint32_t tiles, int xwidth,
                      uint32_t* err) {
   using C = Config<XT, NT, RT>;
   constexpr int PARTS = C::kParts;
@@ -259,16 +286,24 @@ __global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
       uint4 x[kUnits][NT][PARTS];
       {
         const int k0 = (kb_lo + b) * 128;
-        if (xvec && k0 + 128 <= K) {
+        auto whole = [&](auto width) {
           Eight<XT> v[kUnits][NT];
 #pragma unroll
           for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) v[u][j].load16(xrow[j] + k0 + 32 * u, 8 * j + gr < p.M);
+            for (int j = 0; j < NT; ++j)
+              v[u][j].template load_whole<decltype(width)::value>(xrow[j] + k0 + 32 * u, 8 * j + gr < p.M);
 #pragma unroll
           for (int u = 0; u < kUnits; ++u)
 #pragma unroll
             for (int j = 0; j < NT; ++j) v[u][j].template pairs<PARTS>(x[u][j]);
+        };
+        if (k0 + 128 <= K && xwidth == 16) {
+          whole(Width<16>());
+        } else if (k0 + 128 <= K && (sizeof(XT) == 4 || xwidth == 4)) {
+          whole(Width<4>());
+        } else if (k0 + 128 <= K) {
+          if constexpr (sizeof(XT) == 2) whole(Width<2>());
         } else {
 #pragma unroll
           for (int u = 0; u < kUnits; ++u)
@@ -368,7 +403,15 @@ cudaError_t launch_zero(const Int4Product& p, int sms, uint32_t* err, cudaStream
   CUtensorMap map;
   if (api_map_codes(&map, p.w.q, (p.K + 1) / 2, p.N, p.w.ldq, kInt4BoxBytes, 16 * RT, CU_TENSOR_MAP_SWIZZLE_64B) != BS_OK)
     return cudaErrorInvalidValue;
-  const bool xvec = (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 && (p.ldx * sizeof(XT)) % 16 == 0;
+  // Bytes of a load of activations: 16 where every row starts on such a boundary
+  // (the distance of rows says nothing about a single one), else 4, and 2 for bf16
+  // rows that start between words.  32768 x 8198, contiguous rows, 1 / 16 / 32 rows:
+  // 43 / 66 / 147 us in words, 44 / 77 / 189 as rows that may start between them, 48
+  // / 100 / 569 element by element; rows padded to 16 bytes 43 / 62 / 121.  8197: 43 /
+  // 82 / 217 against 48 / 100 / 534.  (Loads of 8 bytes as well: 129 against 150 for
+  // 32 rows of 8196, but 87 against 78 for 17 fp32 rows of 8208.)
+  const uintptr_t starts = reinterpret_cast<uintptr_t>(p.x) | (p.M > 1 ? static_cast<uintptr_t>(p.ldx) * sizeof(XT) : 0);
+  const int xwidth = starts % 16 == 0 ? 16 : (starts % 4 == 0 ? 4 : 2);
   const long long blocks = (p.K + 127) / 128;
   int kw = 1;  // warps that split K: all eight where there are as many blocks
   while (kw < kWarps && 2 * kw <= blocks) kw *= 2;
@@ -385,7 +428,7 @@ cudaError_t launch_zero(const Int4Product& p, int sms, uint32_t* err, cudaStream
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemv_int4_kernel<XT, GPB, NT, RT, ZERO>, map, p, kw, static_cast<uint32_t>(tiles), xvec, err);
+  return cudaLaunchKernelEx(&cfg, gemv_int4_kernel<XT, GPB, NT, RT, ZERO>, map, p, kw, static_cast<uint32_t>(tiles), xwidth, err);
 }
 
 template <typename XT, int GPB, int NT, int RT>

@@ -293,6 +293,60 @@ def test_product_views_vectors_and_untouched_output():
     assert same(bs.bs_gemv_int4(x, dev[0], sc[:, 1:5], group=group, out_dtype=F), bs.bs_gemv_int4(x, *dev, group=group, out_dtype=F))
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("M", [1, 2, 8, 13, 32])
+@pytest.mark.parametrize("N", [70, 5000])
+def test_product_activation_rows_on_every_boundary(N, M, dtype):
+    """Rows that start 16, 8, 4 and 2 bytes off a boundary, together or in turn, give the bits of aligned rows, and no
+    neighbour of a row is taken for one of its elements."""
+    K, group = 430, 64  # whole blocks and a ragged one
+    host, dev = _matrix(N, K, group, 6)
+    x = torch.randn(M, K, generator=_gen(M + N)).to(dtype)
+    want = _product_check(x, host, dev, group, F, x_dev=_aligned(x))
+    for off, pad in ((0, 1), (1, 0), (1, 1), (0, 2), (2, 0), (2, 4), (3, 3), (4, 4), (4, 8), (8, 8), (7, 16)):
+        flat = torch.full((off + M * (K + pad) + 8,), float("nan"), dtype=dtype, device=DEV)
+        view = flat[off:off + M * (K + pad)].view(M, K + pad)[:, :K]
+        view.copy_(x)
+        assert same(want, bs.bs_gemv_int4(view, *dev, group=group, out_dtype=F)), (off, pad)
+
+
+def _aligned(x):
+    """x on the GPU with rows on 16-byte boundaries."""
+    return bs._empty_out((x.shape[0],), x.shape[1], x.dtype, DEV).copy_(x)
+
+
+def _us(call, reps=20):
+    """The least time of a call among others, on the device."""
+    graph = torch.cuda.CUDAGraph()
+    call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for _ in range(8):
+            call()
+    times = []
+    for _ in range(reps):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        graph.replay()
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end))
+    return min(times) * 1e3 / 8
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("K", [4100, 4098, 4097])
+def test_product_activation_rows_off_boundaries_cost_no_multiple(K):
+    """Contiguous rows of a length that is no multiple of 16 bytes: 1.2 to 1.8 times aligned rows' time (element by
+    element they took four times)."""
+    M, N = 32, 32768
+    _, dev = _matrix(N, K, 128, 6)
+    x = torch.randn(M, K, generator=_gen(1)).to(BF)
+    out = torch.empty(M, N, dtype=BF, device=DEV)
+    times = [_us(lambda x=x: bs.bs_gemv_int4(x, *dev, out=out)) for x in (_aligned(x), x.to(DEV))]
+    assert times[1] <= 2.5 * times[0], times
+
+
 def test_binding_refusals():
     host, dev = _matrix(8, 128, 64, 1)
     x = torch.randn(2, 128, device=DEV)
