@@ -665,6 +665,74 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.slow
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("T", [5, 700, 9000])
+def test_gradient_offsets_past_32_bits_in_every_row(T, accumulate):
+    """A gradient of 2.2e9 elements by each of the three sorts, every row looked at: small integers, so that sums are exact,
+    and tokens on both sides of 2^31 elements, the last rows named by more than a chunk of them."""
+    V, D = 270000, 8192
+    g = _gen(T)
+    tokens = torch.randint(0, V, (T,), generator=g)
+    near = torch.tensor([V - 1, V - 3, 0, V - 2, V - 1, 2**18 - 1, 2**18])  # row 2^18 begins at element 2^31
+    tokens[::2] = near[torch.randint(0, len(near), (len(tokens[::2]),), generator=g)]
+    tokens = tokens.to(DEV)
+    grad = torch.randint(-8, 9, (T, D), generator=g).float().to(DEV)
+    d = torch.full((V, D), 3.0, device=DEV)
+    bs.bs_embedding_grad(tokens, grad, V, out=d, accumulate=accumulate)
+    rows, place = torch.unique(tokens, return_inverse=True)
+    sums = torch.zeros(len(rows), D, device=DEV).index_add_(0, place, grad)
+    rest = 3.0 if accumulate else 0.0
+    for r, want in zip(rows.tolist(), sums + rest):
+        assert torch.equal(d[r], want), r
+        d[r] = rest
+    for lo in range(0, V, 16384):
+        assert torch.all(d[lo:lo + 16384] == rest), lo
+
+
+@pytest.mark.slow
+def test_lookup_output_past_32_bits():
+    T, V, D = 270000, 50, 8192  # 2.2e9 elements of output
+    tokens = torch.randint(-1, V + 1, (T,), generator=_gen(1)).to(DEV)
+    for fmt in ("bf16", "int4"):
+        values, table, kw = _table(fmt, V, D, 3)
+        want = torch.cat([torch.from_numpy(values).to(BF), torch.zeros(1, D, dtype=BF)]).to(DEV)
+        row = torch.where((tokens >= 0) & (tokens < V), tokens, V)
+        out = bs.bs_embedding(tokens, table, **kw)
+        for lo in range(0, T, 16384):
+            assert torch.equal(out[lo:lo + 16384], want[row[lo:lo + 16384]]), (fmt, lo)
+        del out
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("N,M", [(2200, 32), (5000, 9)])
+def test_wide_row_strides_past_32_bits(N, M):
+    """Inputs and outputs whose rows lie so far apart that the last ones are past 2^32 bytes, against dense ones: the
+    quantiser, the dequantiser, the lookup and the product (both sizes of its row tiles)."""
+    K, group = 260, 32
+    G = -(-K // group)
+
+    def far(rows, cols, dtype, like=None):
+        ld = -(-(2**32 // dtype.itemsize) // (rows - 1) // 64) * 64 + 256  # the last row begins past 2^32 bytes
+        t = torch.empty(rows * ld, dtype=dtype, device=DEV).view(rows, ld)[:, 5 * 16 // dtype.itemsize:][:, :cols]
+        assert (rows - 1) * ld * dtype.itemsize > 2**32
+        return t if like is None else t.copy_(like)
+
+    x = _weights(N, K, 3).to(DEV)
+    near = bs.bs_quantize_int4(x, group=group, asymmetric=True)
+    q, s, z = bs.bs_quantize_int4(far(N, K, BF, x), group=group, asymmetric=True, q=far(N, K // 2, torch.uint8),
+                                  scale=far(N, G, F), zero=far(N, G, torch.uint8))
+    for a, b in zip((q, s, z), near):
+        assert same(a, b)
+    dense = bs.bs_dequantize_int4(*near, group=group)
+    assert same(bs.bs_dequantize_int4(q, s, z, group=group, out=far(N, K, BF)), dense)
+    tokens = torch.arange(N - 1, -1, -1, device=DEV)
+    assert same(bs.bs_embedding(tokens, q, s, z, format="int4", group=group, out=far(N, K, BF)), dense.flip(0))
+    act = torch.randn(M, K, generator=_gen(4)).to(BF).to(DEV)
+    want = bs.bs_gemv_int4(act, *near, group=group)
+    assert same(bs.bs_gemv_int4(far(M, K, BF, act), q, s, z, group=group, out=far(M, N, BF)), want)
+
+
+@pytest.mark.slow
 @pytest.mark.parametrize("T", [300, 1000, 5000])
 def test_gradient_of_a_very_long_table(T):
     """More rows than a CTA marks at a time; small integers, so that every sum is exact."""
