@@ -393,7 +393,8 @@ bs_status bs_quantize_fp8_128x128(const void* x, bs_in_dtype x_dtype, int64_t R,
  * bs_dequantize_int4 writes the values, out[n, k] = scale * (c - zero) rounded
  * to fp32 and then to the output type (BS_OUT_BF16 or BS_OUT_F32, row stride
  * ldo elements): the operand of a library product when there are more rows
- * than bs_gemv_int4 takes.  K is below 2^30.
+ * than bs_gemv_int4 takes.  K is below 2^30, and the output has fewer than 2^43
+ * elements, K counted up to a multiple of 4.
  */
 bs_status bs_quantize_int4(const void* x, bs_in_dtype x_dtype, int64_t N, int64_t K, int64_t ldx, void* q, int64_t ldq,
                            void* scale, bs_in_dtype scale_dtype, int64_t ld_scale, uint8_t* zero, int64_t ld_zero,
@@ -417,7 +418,7 @@ bs_status bs_dequantize_int4(const void* q, int64_t ldq, const void* scale, bs_i
  *   q      codes [N, K] as above, 16-byte aligned with ldq a multiple of 16
  *   bias   fp32 [N] or NULL
  *   out    [M, N], row stride ldo (>= N), BS_OUT_BF16 or BS_OUT_F32
- * K is below 2^30 and ldq below 2^40.  M == 0 or N == 0 is a no-op; K == 0
+ * N and K are below 2^30 and ldq below 2^40.  M == 0 or N == 0 is a no-op; K == 0
  * writes the bias, or zeros.
  */
 bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const void* q, int64_t ldq, const void* scale,
@@ -455,8 +456,9 @@ bs_status bs_gemv_int4(const void* x, bs_in_dtype x_dtype, int64_t ldx, const vo
  *            bytes, and NULL, for up to 512 tokens);
  *            its contents need not be set and mean nothing afterwards.  Calls
  *            that overlap on the GPU need a workspace each.
- * T and V are below 2^31, D below 2^30.  Pointers are aligned to their element sizes (rows
- * on 16-byte boundaries are faster).  T == 0 or D == 0 looks nothing up; the
+ * T and V are below 2^31, D below 2^30, and an output [rows, D] has fewer than 2^43
+ * elements, D counted up to a multiple of 4.  Pointers are aligned to their element
+ * sizes (rows on 16-byte boundaries are faster).  T == 0 or D == 0 looks nothing up; the
  * gradient of T == 0 is zero.
  */
 typedef enum {

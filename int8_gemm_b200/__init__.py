@@ -696,7 +696,8 @@ def bs_quantize_int4(x: torch.Tensor, group: int = 128, scale_dtype: torch.dtype
 def bs_dequantize_int4(q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None, K: int | None = None,
                        group: int = 128, out_dtype: torch.dtype = torch.bfloat16,
                        out: torch.Tensor | None = None) -> torch.Tensor:
-    """The values [N, K] of a 4-bit matrix (bs_quantize_int4), scale * (code - zero), as bfloat16 or float32.
+    """The values [N, K] of a 4-bit matrix (bs_quantize_int4), scale * (code - zero), as bfloat16 or float32; zero
+    points lie in 0 .. 15.
     K is twice q's columns unless given (an odd K leaves the last byte's high nibble unused)."""
     index = _same_device(q, scale, zero)
     K = 2 * q.shape[-1] if K is None else int(K)
@@ -715,7 +716,7 @@ def bs_gemv_int4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, zero: to
     x     bfloat16 or float32 [M, K], M <= 32, or [K] (then out is [N])
     q, scale, zero  W [N, K] as bs_quantize_int4 makes it, rows of q on 16-byte boundaries
     bias  float32 [N] or None;  out_dtype bfloat16 or float32
-    Sums are fp32, and neither weights nor activations are rounded on the way.
+    Sums are fp32, and neither weights nor activations (fp32 ones from 2^-100 up) are rounded on the way.
     """
     index = _same_device(x, q, scale, zero, bias)
     x2 = x if x.dim() != 1 else x.unsqueeze(0)

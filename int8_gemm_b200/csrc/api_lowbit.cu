@@ -61,7 +61,8 @@ bs_status check_rows_out(const void* out, bs_out_dtype out_dtype, int64_t ldo, i
   if (!extent_ok(T, ldo, 4)) return api_fail(BS_ERR_LAYOUT, "a stride times the number of rows is out of range");
   if (!aligned(out, out_size(out_dtype))) return api_fail(BS_ERR_ALIGNMENT, "out must be aligned to its element size");
   if (D > (kMaxDim >> 1)) return api_fail(BS_ERR_SHAPE, "rows of more than 2^30-1 elements");
-  if (T * ((D + 3) / 4) / 1024 >= kMaxDim) return api_fail(BS_ERR_SHAPE, "more than 2^42 elements");
+  if (T * ((D + 3) / 4) / 1024 >= kMaxDim)
+    return api_fail(BS_ERR_SHAPE, "rows of %lld elements, %lld of them: about 2^43 elements or more", (long long)D, (long long)T);
   return BS_OK;
 }
 

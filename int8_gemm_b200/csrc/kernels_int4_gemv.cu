@@ -24,11 +24,13 @@
 // way.  The four lanes of a row load four consecutive groups' scales and zero
 // points at once, one span of blocks ahead, and pass them round by shuffles.
 //
-// What bounds it: not memory but the issue of a warp's dependent instructions.
-// A word of 8 codes costs 11 operations to unpack (3 shifts, 4 three-input
-// logical, 4 bf16 subtractions, all at half rate), NT MMAs of 8 pipe cycles and
-// about 8 more for activations, scales, sums and the ring.  131072 x 5120, groups
-// of 128, bf16: one row 86 us, 16 rows 125, where the copies alone take 52.
+// What bounds it: latency, with few warps to cover it.  A word of 8 codes costs 26
+// warp instructions at 16 rows (11 unpack it: 3 shifts, 4 three-input logical, 4
+// bf16 subtractions; the others are MMAs, activations, scales, sums and the ring),
+// which 131072 x 5120 in groups of 128 could issue in 66 us; but fragments, sums and
+// scales take 128 registers, so an SM holds 16 warps, and they issue in 54 % of the
+// cycles, no pipe above 50 %.  One row takes 85 us, 16 rows 125, 32 rows (8 warps on
+// an SM) 266, where the copies alone take 52.
 #include <cuda_bf16.h>
 
 #include "lowbit.h"
@@ -155,8 +157,9 @@ struct Eight {
 
 // GPB: groups per 128-deep block (1, 2 or 4); NT: tiles of 8 activation rows;
 // RT: 16-row tiles of the matrix per warp; ZERO: the matrix has zero points.
-// The ring is as deep as leaves room for kCtas CTAs on an SM (a third stage that
-// cost the second CTA: 128 us in place of 101 on 131072 x 5120, one row).
+// The ring is as deep as leaves room for kCtas CTAs on an SM (a third stage of 64
+// rows, which cost the second CTA: 131072 x 5120, one row 101 us in place of 85, 16
+// rows 157 in place of 125).
 template <typename XT, int NT, int RT>
 struct Config {
   static constexpr int kParts = sizeof(XT) == 2 ? 1 : 3;
@@ -437,11 +440,22 @@ cudaError_t launch_one(const Int4Product& p, int sms, uint32_t* err, cudaStream_
 }
 
 // Rows per warp: 64 (32 with four tiles of activation rows, whose fragments take
-// the registers) share a block's activations, 16 give more CTAs.  Measured,
-// 64 against 16: 7168 x 2048, 8 rows 6.9 against 8.2 us; 131072 x 5120, one row
-// 86 against 135; 2900 x 1500 7.6 against 6.2; 1024 x 4096 8.0 against 5.5.
-// fp32 activations, split in registers, pay for 64 rows earlier: 8191 x 8208,
-// 5 rows 30 against 64.
+// the registers) share a block's activations, 16 give more CTAs; fp32 activations,
+// split in registers, pay for 64 earlier.  Many rows / 16, us, groups of 128:
+//   bf16, K = 4096   1 row       8 rows      16 rows     32 rows
+//     N = 2048       7.9 / 5.5   8.8 / 6.4   11.1 / 6.8  10.4 / 8.7
+//     N = 4736       8.5 / 9.7   9.5 / 9.9   11.9 / 8.8  11.2 / 15.5
+//     N = 8192       9.5 / 13.2  10.7 / 13.7 12.9 / 14.1 19.3 / 27.9
+//     131072 x 5120  85 / 133                125 / 192   267 / 423
+//   fp32, K = 4096
+//     N = 2048       12.5 / 9.1  14.0 / 10.5 21.0 / 14.6
+//     N = 2368       12.6 / 9.3  14.0 / 10.7 21.1 / 14.7
+//     N = 4096       13.0 / 15.4 14.5 / 16.8 21.6 / 25.5
+//     N = 8192       14.1 / 28.1 15.8 / 29.7 22.8 / 48.4
+// The rule looks at N alone.  Where K is short, so that fewer warps share it and a
+// CTA takes up to 512 rows, 16 stay ahead for longer: 5000 x 128 3.0 / 2.4, 3.9 /
+// 2.7, 5.3 / 3.3, 5.6 / 4.2; 8192 x 256 3.0 / 2.6, 4.4 / 3.0, 6.7 / 3.5, 6.3 / 4.7;
+// 16384 x 512 3.8 / 5.0, 4.5 / 5.5, 6.0 / 6.4, 9.3 / 11.8.
 template <typename XT, int GPB, int NT>
 cudaError_t launch_rows(const Int4Product& p, int sms, uint32_t* err, cudaStream_t stream) {
   constexpr int RT = NT == 4 ? 2 : 4;

@@ -249,8 +249,8 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 // A CTA places kRankTokens pairs: a pair's place is the number of pairs before
 // it, counted over all tokens by kRankWays threads per pair.  Keys are below
 // 2^24 and compared as fp32 integers: the saturated difference bound - k is 1
-// where k < bound and 0 elsewhere, one full-rate operation where an integer
-// comparison and its count take three of half rate.
+// where k < bound and 0 elsewhere, so a comparison and its count are two
+// full-rate operations, a difference and an addition.
 __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   constexpr int kTile = 2048, kLoads = kTile / kThreads, kPart = kTile / kRankWays;
   __shared__ float4 tile[kTile / 4];

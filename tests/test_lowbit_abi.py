@@ -127,6 +127,18 @@ def test_embedding_refusals():
             assert _emb(**kw) == bs.BS_ERR_DEVICE, kw
 
 
+def test_outputs_below_2_to_the_43_elements():
+    """Rows times columns, the columns counted up to a multiple of 4."""
+    for call in (lambda rows, cols: _emb(T=rows, D=cols, ld=cols, ldo=cols),
+                 lambda rows, cols: _deq(N=rows, K=cols, ldq=cols, lds=cols, ldo=cols),
+                 lambda rows, cols: _grad(V=rows, D=cols, ldg=cols, ldd=cols, n=1 << 62)):
+        assert call(1 << 29, 1 << 14) == bs.BS_ERR_SHAPE
+        assert "2^43" in bs.lib().bs_last_error_message().decode()
+        assert call(1 << 30, (1 << 13) - 3) == bs.BS_ERR_SHAPE
+        if not HAS_GPU:
+            assert call((1 << 29) - 1, 1 << 14) == bs.BS_ERR_DEVICE
+
+
 def _grad(**kw):
     a = dict(tok=P, td=1, T=2000, grad=P, gd=0, ldg=300, V=50, D=300, alpha=1.0, pad=-1, d=P, od=1, ldd=300, acc=0, ws=P,
              n=None)
