@@ -303,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, Config<XT, NT, RT>::kCtas)
         };
         if (k0 + 128 <= K && xwidth == 16) {
           whole(Width<16>());
-        } else if (k0 + 128 <= K && (sizeof(XT) == 4 || xwidth == 4)) {
+        } else if (k0 + 128 <= K && (sizeof(XT) == 4 ? RT > 1 : xwidth == 4)) {
           whole(Width<4>());
-        } else if (k0 + 128 <= K) {
+        } else if (sizeof(XT) == 2 && k0 + 128 <= K) {
           if constexpr (sizeof(XT) == 2) whole(Width<2>());
         } else {
 #pragma unroll
@@ -412,7 +412,10 @@ cudaError_t launch_zero(const Int4Product& p, int sms, uint32_t* err, cudaStream
   // 43 / 66 / 147 us in words, 44 / 77 / 189 as rows that may start between them, 48
   // / 100 / 569 element by element; rows padded to 16 bytes 43 / 62 / 121.  8197: 43 /
   // 82 / 217 against 48 / 100 / 534.  (Loads of 8 bytes as well: 129 against 150 for
-  // 32 rows of 8196, but 87 against 78 for 17 fp32 rows of 8208.)
+  // 32 rows of 8196, but 87 against 78 for 17 fp32 rows of 8208.)  fp32, whose split
+  // needs the registers, goes by words where a warp has 64 matrix rows (8192 x 4098, 9
+  // rows 27.9 against 29.0) and word by word, each eight split before the next are
+  // read, where it has 16 (179 x 8982, 9 rows 28.2 against 32.5).
   const uintptr_t starts = reinterpret_cast<uintptr_t>(p.x) | (p.M > 1 ? static_cast<uintptr_t>(p.ldx) * sizeof(XT) : 0);
   const int xwidth = starts % 16 == 0 ? 16 : (starts % 4 == 0 ? 4 : 2);
   const long long blocks = (p.K + 127) / 128;
